@@ -14,7 +14,9 @@
  *   moe_grouped_ffn_mxfp4  -> y_sorted   (W1 gate|up, clamped SwiGLU, W2)
  *   moe_combine            -> y
  * moe_route_and_group runs the first three as one call (one launch for small T);
- * moe_forward_mxfp4 runs all five.
+ * moe_forward_mxfp4 runs all five.  moe_route_scored takes moe_route's place for
+ * routers with scores, a balance bias and expert groups, and moe_fp8.h has the
+ * grouped FFN over block-scaled FP8 weights; the other steps are the same.
  *
  * Conventions shared by every call
  *   - Every pointer argument is a DEVICE pointer (memory the GPU can read or
@@ -194,6 +196,63 @@ moe_status moe_route_and_group(const float* logits, int64_t T, int32_t E, int32_
                                int32_t* topk_ids, float* topk_weights, uint32_t* bitmatrix,
                                int32_t* counts, int32_t* offsets, int32_t* gather,
                                int32_t* scatter, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_route_scored -- top-k selection over expert scores, with a balance bias,
+ * expert groups and renormalised weights.
+ *
+ * Per token, with logits l_e:
+ *   score  s_e = exp(l_e - m) / sum_i exp(l_i - m), m = max_i l_i   (MOE_SCORE_SOFTMAX)
+ *          s_e = 1 / (1 + exp(-l_e))                                (MOE_SCORE_SIGMOID)
+ *   key    s_e + bias_e (bias NULL: s_e); keys order the experts, scores weigh them
+ *   groups expert e belongs to group e / (E / groups).  A group's key is its
+ *          largest expert key (group_top 1) or the sum of its two largest
+ *          (group_top 2; a group of one expert: that one).  Only experts of the
+ *          topk_groups groups with the largest group keys can be chosen.
+ *          groups = 1: every expert can.
+ *   topk_ids[t][0..k-1]   the k largest keys, key descending
+ *   topk_weights[t][j]    scale * s_(chosen j), with renormalize != 0 divided by
+ *                         the sum of the k chosen scores (0 if that sum is 0)
+ * Equal keys, of experts or of groups, go to the lower index.  Keys are ordered
+ * as in 64-bit arithmetic: keys that fp32 cannot tell apart are compared again
+ * in fp64.  Without a bias, experts are ordered by their logits, whose order
+ * the scores share.
+ *
+ * A logit of -inf or NaN excludes its expert: score 0, ranked after every other
+ * expert of an eligible group and not counted in its group's key (a group whose
+ * experts are all excluded ranks last).  If fewer than k experts are left, the
+ * remaining slots hold excluded experts of eligible groups, lower index first,
+ * with weight 0.  A logit of +inf has score 1 (softmax: the +inf logits share 1
+ * equally).  The type's lowest finite value is an ordinary logit.
+ *
+ *   logits        fp32 or bf16 [T][E], by logits_type; aligned to its elements
+ *   bias          fp32 [E], finite, or NULL
+ *   topk_ids      int32 [T][k]   out
+ *   topk_weights  fp32  [T][k]   out
+ * groups must divide E and be at most 64; 1 <= topk_groups <= groups; group_top
+ * is 1 or 2; k <= topk_groups * (E / groups).  T = 0 enqueues nothing.
+ */
+typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+typedef enum moe_score { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score;
+
+moe_status moe_route_scored(const void* logits, int32_t logits_type, int64_t T, int32_t E,
+                            int32_t k, int32_t score, const float* bias, int32_t groups,
+                            int32_t topk_groups, int32_t group_top, int32_t renormalize,
+                            float scale, int32_t* topk_ids, float* topk_weights, void* stream);
+
+/*
+ * moe_route_scored_and_group -- moe_route_scored, moe_build_bitmatrix and
+ * moe_expert_offsets in one call, with exactly their outputs (one launch for
+ * T <= 64, as moe_route_and_group).  ws is the workspace of moe_expert_offsets.
+ * T = 0 writes zeros to counts and offsets.
+ */
+moe_status moe_route_scored_and_group(const void* logits, int32_t logits_type, int64_t T,
+                                      int32_t E, int32_t k, int32_t score, const float* bias,
+                                      int32_t groups, int32_t topk_groups, int32_t group_top,
+                                      int32_t renormalize, float scale, int32_t* topk_ids,
+                                      float* topk_weights, uint32_t* bitmatrix, int32_t* counts,
+                                      int32_t* offsets, int32_t* gather, int32_t* scatter,
+                                      void* ws, size_t ws_bytes, void* stream);
 
 /*
  * moe_forward_mxfp4 -- the whole layer in one call: exactly the outputs of

@@ -21,7 +21,9 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_UNSUPPORTED",
           3: "MOE_ERR_MISALIGNED", 4: "MOE_ERR_WORKSPACE_TOO_SMALL", 5: "MOE_ERR_HIP"}
 
 EXPORTS = ("moe_route", "moe_build_bitmatrix", "moe_expert_offsets", "moe_route_and_group",
-           "moe_grouped_ffn_mxfp4", "moe_combine", "moe_workspace_bytes", "moe_status_string")
+           "moe_grouped_ffn_mxfp4", "moe_combine", "moe_workspace_bytes", "moe_status_string",
+           "moe_route_scored", "moe_route_scored_and_group", "moe_quantize_fp8", "moe_gemm_fp8",
+           "moe_gemm_fp8_workspace_bytes", "moe_grouped_ffn_fp8", "moe_fp8_workspace_bytes")
 
 
 # bf16 buffers may be given as bfloat16 tensors or as int16 tensors of bit patterns
@@ -56,6 +58,17 @@ _SIG = {
                                 ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
                                 ctypes.c_size_t, _P, _P],
     "moe_read_probe": [_P, ctypes.c_size_t, _P, _P],
+    "moe_route_scored": [_P, _I32, _I64, _I32, _I32, _I32, _P, _I32, _I32, _I32, _I32,
+                         ctypes.c_float, _P, _P, _P],
+    "moe_route_scored_and_group": [_P, _I32, _I64, _I32, _I32, _I32, _P, _I32, _I32, _I32, _I32,
+                                   ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, _P,
+                                   ctypes.c_size_t, _P],
+    "moe_quantize_fp8": [_P, _I64, _I32, _P, _P, _P],
+    "moe_gemm_fp8": [_P, _P, _I64, _I32, _I32, _P, _P, _I32, _P, _P, ctypes.c_size_t, _P],
+    "moe_gemm_fp8_workspace_bytes": [_I64, _I32, _I32],
+    "moe_grouped_ffn_fp8": [_P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P,
+                            ctypes.c_float, _P, _P, ctypes.c_size_t, _P],
+    "moe_fp8_workspace_bytes": [_I64, _I32, _I32, _I32, _I32],
     "moe_workspace_bytes": [_I64, _I32, _I32, _I32, _I32],
     "moe_status_string": [ctypes.c_int],
 }
@@ -74,7 +87,8 @@ def load(path: str = LIB_PATH):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
-    lib.moe_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("moe_workspace_bytes", "moe_gemm_fp8_workspace_bytes", "moe_fp8_workspace_bytes"):
+        getattr(lib, name).restype = ctypes.c_size_t
     lib.moe_status_string.restype = ctypes.c_char_p
     _lib = lib
     return lib
@@ -250,3 +264,156 @@ def moe_read_probe(buf, sink, stream=None):
     _check("moe_read_probe", load().moe_read_probe(
         _ptr(buf, None, "buf"), buf.numel() * buf.element_size(), _ptr(sink, torch.int32, "sink"),
         _stream(stream)))
+
+
+# ------------------------------------------------------------ scored routing, block-scaled FP8
+#
+# These calls also check shapes, and that every tensor is on one GPU; they run on that GPU's
+# current stream (or the one given).
+
+# E4M3 buffers may be given as float8_e4m3fn tensors or as uint8 tensors of codes
+E4M3 = (torch.float8_e4m3fn, torch.uint8)
+SCORES = {"softmax": 0, "sigmoid": 1}
+LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+FP8_BLOCK = 128
+
+
+class _Args:
+    """Pointers of one call's tensors, checked: dtype, shape, contiguity, one GPU."""
+
+    def __init__(self):
+        self.device = None
+
+    def ptr(self, t, dtype, shape, name):
+        if t.get_device() != self.device:
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a GPU tensor")
+            if self.device is not None:
+                raise ValueError(f"{name} is on another GPU than the other tensors")
+            self.device = t.get_device()
+        if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def ws(self, t):
+        if t is None:
+            return None, 0
+        return self.ptr(t, torch.uint8, t.shape, "ws"), t.numel()
+
+
+def _run(fn: str, a: _Args, stream, *args):
+    if stream is None:
+        handle = torch.cuda.current_stream(a.device).cuda_stream
+    else:
+        handle = _stream(stream)
+    if a.device == torch.cuda.current_device():
+        code = getattr(load(), fn)(*args, handle)
+    else:
+        with torch.cuda.device(a.device):
+            code = getattr(load(), fn)(*args, handle)
+    _check(fn, code)
+
+
+def _runs(n: int) -> int:
+    return -(-n // FP8_BLOCK)
+
+
+def _scored(a, logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups, group_top,
+            renormalize, scale):
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    if logits.dtype not in LOGIT_TYPES:
+        raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    return (a.ptr(logits, logits.dtype, (T, E), "logits"), LOGIT_TYPES[logits.dtype], T, E, k,
+            SCORES[score], None if bias is None else a.ptr(bias, torch.float32, (E,), "bias"),
+            groups, topk_groups, group_top, 1 if renormalize else 0, scale,
+            a.ptr(topk_ids, torch.int32, (T, k), "topk_ids"),
+            a.ptr(topk_weights, torch.float32, (T, k), "topk_weights"))
+
+
+def moe_route_scored(logits, k: int, topk_ids, topk_weights, *, score: str = "softmax", bias=None,
+                     groups: int = 1, topk_groups: int = 1, group_top: int = 2,
+                     renormalize: bool = True, scale: float = 1.0, stream=None):
+    """Top-k over softmax or sigmoid scores plus a balance bias, within the best expert groups;
+    weights are the chosen scores, renormalised or not, times `scale`."""
+    a = _Args()
+    _run("moe_route_scored", a, stream,
+         *_scored(a, logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups,
+                  group_top, renormalize, scale))
+
+
+def moe_route_scored_and_group(logits, k: int, topk_ids, topk_weights, bitmatrix, counts, offsets,
+                               gather, scatter, ws, *, score: str = "softmax", bias=None,
+                               groups: int = 1, topk_groups: int = 1, group_top: int = 2,
+                               renormalize: bool = True, scale: float = 1.0, stream=None):
+    """moe_route_scored, moe_build_bitmatrix and moe_expert_offsets in one call."""
+    a = _Args()
+    how = _scored(a, logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups,
+                  group_top, renormalize, scale)
+    T, E = logits.shape
+    i32 = torch.int32
+    _run("moe_route_scored_and_group", a, stream, *how,
+         a.ptr(bitmatrix, i32, (T, (E + 31) // 32), "bitmatrix"), a.ptr(counts, i32, (E,), "counts"),
+         a.ptr(offsets, i32, (E + 1,), "offsets"), a.ptr(gather, i32, (T * k,), "gather"),
+         a.ptr(scatter, i32, (T * k,), "scatter"), *a.ws(ws))
+
+
+def moe_quantize_fp8(x, q, scale, stream=None):
+    """bf16 rows [rows, K] to E4M3 codes q [rows, K] with scale [rows, ceil(K / 128)]."""
+    a = _Args()
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, K]")
+    rows, K = x.shape
+    _run("moe_quantize_fp8", a, stream, a.ptr(x, BF16, (rows, K), "x"), rows, K,
+         a.ptr(q, E4M3, (rows, K), "q"), a.ptr(scale, torch.float32, (rows, _runs(K)), "scale"))
+
+
+def moe_gemm_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
+    return int(load().moe_gemm_fp8_workspace_bytes(M, N, K))
+
+
+def moe_gemm_fp8(xq, x_scale, w, w_scale, y, ws=None, stream=None):
+    """y [M, N] (bf16 or fp32) = X W^T of block-scaled E4M3 xq [M, K] and w [N, K]; ws holds
+    moe_gemm_fp8_workspace_bytes(M, N, K) bytes (None where that is 0)."""
+    a = _Args()
+    if xq.dim() != 2 or w.dim() != 2:
+        raise ValueError("xq must be [M, K] and w [N, K]")
+    M, K = xq.shape
+    N = w.shape[0]
+    kind = 0 if y.dtype == torch.float32 else 1
+    _run("moe_gemm_fp8", a, stream, a.ptr(xq, E4M3, (M, K), "xq"),
+         a.ptr(x_scale, torch.float32, (M, _runs(K)), "x_scale"), M, N, K,
+         a.ptr(w, E4M3, (N, K), "w"),
+         a.ptr(w_scale, torch.float32, (_runs(N), _runs(K)), "w_scale"), kind,
+         a.ptr(y, torch.float32 if kind == 0 else BF16, (M, N), "y"), *a.ws(ws))
+
+
+def moe_fp8_workspace_bytes(T: int, E: int, k: int, H: int, I: int) -> int:
+    return int(load().moe_fp8_workspace_bytes(T, E, k, H, I))
+
+
+def moe_grouped_ffn_fp8(x, k: int, w1, w1_scale, w2, w2_scale, counts, offsets, gather,
+                        swiglu_limit: float, y_sorted, ws, stream=None):
+    """The grouped expert FFN over block-scaled E4M3 weights w1 [E, 2I, H] (gate rows, then up
+    rows) and w2 [E, H, I]; ws holds moe_fp8_workspace_bytes(T, E, k, H, I) bytes."""
+    a = _Args()
+    if x.dim() != 2 or w1.dim() != 3 or w1.shape[1] % 2:
+        raise ValueError("x must be [T, H] and w1 [E, 2I, H]")
+    T, H = x.shape
+    E, I = w1.shape[0], w1.shape[1] // 2
+    f32, i32 = torch.float32, torch.int32
+    _run("moe_grouped_ffn_fp8", a, stream, a.ptr(x, BF16, (T, H), "x"), T, H, I, E, k,
+         a.ptr(w1, E4M3, (E, 2 * I, H), "w1"),
+         a.ptr(w1_scale, f32, (E, _runs(2 * I), _runs(H)), "w1_scale"),
+         a.ptr(w2, E4M3, (E, H, I), "w2"),
+         a.ptr(w2_scale, f32, (E, _runs(H), _runs(I)), "w2_scale"),
+         a.ptr(counts, i32, (E,), "counts"), a.ptr(offsets, i32, (E + 1,), "offsets"),
+         a.ptr(gather, i32, (T * k,), "gather"), float(swiglu_limit),
+         a.ptr(y_sorted, BF16, (T * k, H), "y_sorted"), *a.ws(ws))

@@ -9,6 +9,7 @@
 // bf16 MFMAs, bound by HBM.  Many rows: the tiled kernels (ffn_tile.hip),
 // block-scaled FP4 x FP8 MFMAs on an LDS activation tile.
 #include "ffn_common.h"
+#include "fp8.h"
 #include "launch.h"
 #include "plan.h"
 #include "validate.h"
@@ -37,6 +38,14 @@ __global__ __launch_bounds__(1024) void plan_kernel(const int32_t* __restrict__ 
 
 }  // namespace
 
+hipError_t launch_plan(const int32_t* counts, const int32_t* offsets, int E, int tile_rows,
+                       int64_t n_slots, int64_t tile_bound, int32_t* n_tiles, RowTile* tiles,
+                       hipStream_t stream) {
+  plan_kernel<<<1, 1024, 0, stream>>>(counts, offsets, E, tile_rows, n_slots, tile_bound, n_tiles,
+                                      tiles);
+  return hipGetLastError();
+}
+
 hipError_t launch_ffn(const uint16_t* x, int64_t T, int H, int I, int E, int k,
                       const uint8_t* w1, const uint8_t* w1s, const uint8_t* w2,
                       const uint8_t* w2s, const int32_t* counts, const int32_t* offsets,
@@ -64,9 +73,7 @@ hipError_t launch_ffn(const uint16_t* x, int64_t T, int H, int I, int E, int k,
 
   hipError_t err = hipSuccess;
   if (!plan_ready) {
-    plan_kernel<<<1, 1024, 0, stream>>>(counts, offsets, E, tile_rows, n_slots, tile_bound,
-                                        n_tiles, tiles);
-    err = hipGetLastError();
+    err = launch_plan(counts, offsets, E, tile_rows, n_slots, tile_bound, n_tiles, tiles, stream);
     if (err != hipSuccess) return err;
   }
   const bool tiled = tile_rows >= 80;

@@ -14,20 +14,11 @@
 // (moe_forward_mxfp4), which saves the FFN its plan launch.  Larger batches run
 // the routing kernel, which then also writes the bit matrix, and the offsets
 // kernels of the separate call.
-#include "config.h"
+#include "group_core.h"
 #include "launch.h"
-#include "routing_core.h"
 
 namespace moe {
 namespace {
-
-constexpr int kFrontMaxTokens = 64;
-
-__device__ __forceinline__ void wave_sync_lds() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-}
 
 template <int EPL>
 __global__ __launch_bounds__(1024) void frontend_small_kernel(
@@ -35,10 +26,7 @@ __global__ __launch_bounds__(1024) void frontend_small_kernel(
     float* __restrict__ weights, uint32_t* __restrict__ bm, int32_t* __restrict__ counts,
     int32_t* __restrict__ offsets, int32_t* __restrict__ gather, int32_t* __restrict__ scatter,
     int tile_rows, int tile_bound, int32_t* __restrict__ n_tiles, RowTile* __restrict__ tiles) {
-  __shared__ int ids_lds[kFrontMaxTokens * kMaxK];
-  __shared__ uint32_t rows_lds[kFrontMaxTokens * (kMaxE / 32)];
-  __shared__ uint64_t masks[kMaxE];
-  __shared__ int off_lds[kMaxE];
+  __shared__ FrontLds lds;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int n_waves = blockDim.x >> 6;
 
@@ -50,96 +38,11 @@ __global__ __launch_bounds__(1024) void frontend_small_kernel(
     if (lane < k) {
       ids[t * k + lane] = id;
       weights[t * k + lane] = w;
-      ids_lds[t * k + lane] = id;
+      lds.ids[t * k + lane] = id;
     }
   }
-  for (int i = threadIdx.x; i < T * words; i += blockDim.x) rows_lds[i] = 0u;
-  __syncthreads();
-
-  // 2. bit matrix: entries past T*k are padding lanes of the logical block
-  const int n_entries = T * k;
-  if (static_cast<int>(threadIdx.x) < n_entries) {
-    const int e = ids_lds[threadIdx.x];
-    if (static_cast<unsigned>(e) < static_cast<unsigned>(E))
-      atomicOr(&rows_lds[(threadIdx.x / k) * words + (e >> 5)], 1u << (e & 31));
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < T * words; i += blockDim.x) bm[i] = rows_lds[i];
-
-  // 3. expert column masks, 64 experts per wavefront (lane = token), then counts,
-  // offsets and permutations in wavefront 0
-  for (int w0 = 2 * wave; w0 < words; w0 += 2 * n_waves)
-    column_masks_64(rows_lds, lane, lane < T, E, words, lane, masks, w0);
-  __syncthreads();
-  if (wave != 0) return;
-  int c[EPL];
-  int sum = 0;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane * EPL + i;
-    c[i] = e < E ? __popcll(masks[e]) : 0;
-    sum += c[i];
-  }
-  int incl = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += o;
-  }
-  int run = incl - sum;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = lane * EPL + i;
-    if (e < E) {
-      counts[e] = c[i];
-      offsets[e] = run;
-      off_lds[e] = run;
-    }
-    run += c[i];
-  }
-  if (lane == 63) offsets[E] = incl;
-  if (tiles != nullptr) {
-    // the FFN's row-tile plan (same tiles and order as its plan kernel): expert e
-    // cut into ceil(count / tile_rows) tiles, experts in index order
-    int nt[EPL], tsum = 0;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      nt[i] = (c[i] + tile_rows - 1) / tile_rows;
-      tsum += nt[i];
-    }
-    int tincl = tsum;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(tincl, d, 64);
-      if (lane >= d) tincl += o;
-    }
-    int slot = tincl - tsum;
-    int off = incl - sum;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      for (int t = 0; t < nt[i] && slot < tile_bound; ++t, ++slot) {
-        RowTile rt;
-        rt.expert = lane * EPL + i;
-        rt.p_begin = off + t * tile_rows;
-        rt.p_end = (t + 1) * tile_rows < c[i] ? off + (t + 1) * tile_rows : off + c[i];
-        rt.multi = c[i] > tile_rows ? 1 : 0;
-        tiles[slot] = rt;
-      }
-      off += c[i];
-    }
-    if (lane == 63) *n_tiles = tincl < tile_bound ? tincl : tile_bound;
-  }
-  wave_sync_lds();
-  // one lane per (token, choice) entry: its row is the expert's offset plus the
-  // earlier tokens that chose the same expert (bits below the token in its mask)
-  for (int s = lane; s < n_entries; s += 64) {
-    const int e = ids_lds[s];
-    if (static_cast<unsigned>(e) >= static_cast<unsigned>(E)) continue;
-    const int p = off_lds[e] + __popcll(masks[e] & ((1ull << (s / k)) - 1ull));
-    if (p < 0 || p >= n_entries) continue;
-    gather[p] = s;
-    scatter[s] = p;
-  }
+  group_small<EPL>(lds, T, E, k, words, bm, counts, offsets, gather, scatter, tile_rows, tile_bound,
+                   n_tiles, tiles);
 }
 
 }  // namespace

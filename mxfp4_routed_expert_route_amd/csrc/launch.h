@@ -79,6 +79,23 @@ hipError_t launch_route_and_group(const float* logits, int64_t T, int E, int k, 
                                   const PlanOut* plan = nullptr, bool* plan_written = nullptr,
                                   const SplitArgs* split = nullptr, bool* split_done = nullptr);
 
+// Scored routing's choices (moe_route_scored); bias nullptr: none.
+struct ScoredRouting {
+  int score;
+  const float* bias;
+  int groups, topk_groups, group_top, renormalize;
+  float scale;
+};
+// With bm != nullptr, also the bit matrix.
+hipError_t launch_route_scored(const void* logits, bool bf16, int64_t T, int E, int k,
+                               const ScoredRouting& r, int32_t* ids, float* weights, uint32_t* bm,
+                               hipStream_t stream);
+hipError_t launch_route_scored_and_group(const void* logits, bool bf16, int64_t T, int E, int k,
+                                         const ScoredRouting& r, int32_t* ids, float* weights,
+                                         uint32_t* bm, int32_t* counts, int32_t* offsets,
+                                         int32_t* gather, int32_t* scatter, void* ws,
+                                         hipStream_t stream);
+
 // x [rows][K] bf16 -> two-part FP8 rows (xq: [rows][2K] bytes) and their E8M0 block
 // scales (xs: [rows][K/32] bytes), the input form of the tiled FFN kernels.
 hipError_t launch_act_split(const uint16_t* x, int64_t rows, int K, uint8_t* xq, uint8_t* xs,

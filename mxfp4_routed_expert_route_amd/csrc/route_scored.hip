@@ -1,0 +1,146 @@
+// Scored routing (softmax or sigmoid scores, balance bias, expert groups): one wavefront
+// per token (route_scored_token in scored_core.h).  As for plain top-k, up to 64 tokens
+// are routed and grouped by expert in one launch of one workgroup (at most 8 experts per
+// lane); above, the routing kernel also writes the bit matrix and the expert-offsets
+// kernels follow.
+#include "group_core.h"
+#include "launch.h"
+#include "scored_core.h"
+
+namespace moe {
+namespace {
+
+template <int EPL, class Logit>
+__global__ __launch_bounds__(256) void route_scored_kernel(
+    const Logit* __restrict__ logits, int64_t T, int E, int k, ScoreArgs a,
+    int32_t* __restrict__ ids, float* __restrict__ weights, uint32_t* __restrict__ bm) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;   // uniform per wavefront
+  int id;
+  float w;
+  route_scored_token<EPL>(logits + t * E, k, lane, a, id, w);
+  if (lane < k) {
+    ids[t * k + lane] = id;
+    weights[t * k + lane] = w;
+  }
+  if (bm != nullptr) {   // uniform: the token's bit-matrix row, lane w writing word w
+    const int words = (E + 31) / 32;
+    uint32_t word = 0;
+    for (int j = 0; j < k; ++j) {
+      const int e = __shfl(id, j, 64);
+      if ((e >> 5) == lane) word |= 1u << (e & 31);
+    }
+    if (lane < words) bm[t * words + lane] = word;
+  }
+}
+
+template <int EPL, class Logit>
+__global__ __launch_bounds__(1024) void scored_front_kernel(
+    const Logit* __restrict__ logits, int T, int E, int k, ScoreArgs a, int words,
+    int32_t* __restrict__ ids, float* __restrict__ weights, uint32_t* __restrict__ bm,
+    int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ gather,
+    int32_t* __restrict__ scatter) {
+  __shared__ FrontLds lds;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n_waves = blockDim.x >> 6;
+  for (int t = wave; t < T; t += n_waves) {
+    int id;
+    float w;
+    route_scored_token<EPL>(logits + static_cast<int64_t>(t) * E, k, lane, a, id, w);
+    if (lane < k) {
+      ids[t * k + lane] = id;
+      weights[t * k + lane] = w;
+      lds.ids[t * k + lane] = id;
+    }
+  }
+  group_small<EPL>(lds, T, E, k, words, bm, counts, offsets, gather, scatter, 1, 0, nullptr,
+                   nullptr);
+}
+
+ScoreArgs score_args(const ScoredRouting& r, int E) {
+  int g2 = 1;
+  while (g2 < r.groups) g2 *= 2;
+  return ScoreArgs{r.score,       r.bias,      r.groups,      E / r.groups, r.topk_groups,
+                   r.group_top,   r.renormalize, r.scale,     64 / g2};
+}
+
+// At most 32: per / L < 2 E / 64.
+int experts_per_lane(const ScoreArgs& a) { return (a.per + a.lanes - 1) / a.lanes; }
+// One launch up to this many experts per lane: with 16 wavefronts a workgroup has 128
+// registers a lane, and 16 or 32 experts per lane would spill there.
+constexpr int kFrontMaxPerLane = 8;
+
+template <class Logit>
+hipError_t launch_route(const Logit* logits, int64_t T, int E, int k, const ScoreArgs& a,
+                        int32_t* ids, float* weights, uint32_t* bm, hipStream_t stream) {
+  const int epl = experts_per_lane(a);
+  const dim3 grid(static_cast<unsigned>((T + 3) / 4)), block(256);
+#define MOE_ROUTE(EPL) \
+  route_scored_kernel<EPL><<<grid, block, 0, stream>>>(logits, T, E, k, a, ids, weights, bm)
+  if (epl <= 1)
+    MOE_ROUTE(1);
+  else if (epl <= 2)
+    MOE_ROUTE(2);
+  else if (epl <= 4)
+    MOE_ROUTE(4);
+  else if (epl <= 8)
+    MOE_ROUTE(8);
+  else if (epl <= 16)
+    MOE_ROUTE(16);
+  else
+    MOE_ROUTE(32);
+#undef MOE_ROUTE
+  return hipGetLastError();
+}
+
+template <class Logit>
+hipError_t launch_front(const Logit* logits, int T, int E, int k, const ScoreArgs& a, int32_t* ids,
+                        float* weights, uint32_t* bm, int32_t* counts, int32_t* offsets,
+                        int32_t* gather, int32_t* scatter, hipStream_t stream) {
+  const int epl = experts_per_lane(a);
+  const int words = (E + 31) / 32;
+#define MOE_FRONT(EPL)                                                                        \
+  scored_front_kernel<EPL><<<1, 1024, 0, stream>>>(logits, T, E, k, a, words, ids, weights, bm, \
+                                                   counts, offsets, gather, scatter)
+  if (epl <= 1)
+    MOE_FRONT(1);
+  else if (epl <= 2)
+    MOE_FRONT(2);
+  else if (epl <= 4)
+    MOE_FRONT(4);
+  else
+    MOE_FRONT(8);
+#undef MOE_FRONT
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_route_scored(const void* logits, bool bf16, int64_t T, int E, int k,
+                               const ScoredRouting& r, int32_t* ids, float* weights, uint32_t* bm,
+                               hipStream_t stream) {
+  const ScoreArgs a = score_args(r, E);
+  return bf16 ? launch_route(static_cast<const uint16_t*>(logits), T, E, k, a, ids, weights, bm, stream)
+              : launch_route(static_cast<const float*>(logits), T, E, k, a, ids, weights, bm, stream);
+}
+
+hipError_t launch_route_scored_and_group(const void* logits, bool bf16, int64_t T, int E, int k,
+                                         const ScoredRouting& r, int32_t* ids, float* weights,
+                                         uint32_t* bm, int32_t* counts, int32_t* offsets,
+                                         int32_t* gather, int32_t* scatter, void* ws,
+                                         hipStream_t stream) {
+  const ScoreArgs a = score_args(r, E);
+  if (T > kFrontMaxTokens || experts_per_lane(a) > kFrontMaxPerLane) {
+    const hipError_t err = launch_route_scored(logits, bf16, T, E, k, r, ids, weights, bm, stream);
+    if (err != hipSuccess) return err;
+    return launch_offsets(bm, ids, T, E, k, counts, offsets, gather, scatter, ws, stream);
+  }
+  const int t = static_cast<int>(T);
+  return bf16 ? launch_front(static_cast<const uint16_t*>(logits), t, E, k, a, ids, weights, bm,
+                             counts, offsets, gather, scatter, stream)
+              : launch_front(static_cast<const float*>(logits), t, E, k, a, ids, weights, bm,
+                             counts, offsets, gather, scatter, stream);
+}
+
+}  // namespace moe

@@ -33,8 +33,16 @@ class LayerBuffers:
 
     @classmethod
     def allocate(cls, T, E, k, H, I, device="cuda"):
+        return cls._allocate(T, E, k, H, I, device, binding.moe_workspace_bytes(T, E, k, H, I))
+
+    @classmethod
+    def allocate_fp8(cls, T, E, k, H, I, device="cuda"):
+        """Buffers of a layer over block-scaled FP8 weights (run_layer_fp8)."""
+        return cls._allocate(T, E, k, H, I, device, binding.moe_fp8_workspace_bytes(T, E, k, H, I))
+
+    @classmethod
+    def _allocate(cls, T, E, k, H, I, device, ws_bytes):
         dev = torch.device(device)
-        ws_bytes = binding.moe_workspace_bytes(T, E, k, H, I)
         if ws_bytes == 0:
             raise ValueError("invalid layer sizes")
         i32 = dict(dtype=torch.int32, device=dev)
@@ -100,6 +108,17 @@ def run_forward(dev: dict, b: LayerBuffers, limit: float, stream=None):
                               dev["w2_s"], limit, b.topk_ids, b.topk_weights, b.bitmatrix,
                               b.counts, b.offsets, b.gather, b.scatter, b.y_sorted, b.y, b.ws,
                               stream)
+
+
+def run_layer_fp8(dev: dict, b: LayerBuffers, limit: float, stream=None, **scoring):
+    """The layer over block-scaled FP8 expert weights with scored routing (`scoring`: the
+    keyword arguments of binding.moe_route_scored): route and group, grouped FFN, combine."""
+    binding.moe_route_scored_and_group(dev["logits"], b.k, b.topk_ids, b.topk_weights, b.bitmatrix,
+                                       b.counts, b.offsets, b.gather, b.scatter, b.ws,
+                                       stream=stream, **scoring)
+    binding.moe_grouped_ffn_fp8(dev["x"], b.k, dev["w1"], dev["w1_s"], dev["w2"], dev["w2_s"],
+                                b.counts, b.offsets, b.gather, limit, b.y_sorted, b.ws, stream)
+    binding.moe_combine(b.y_sorted, b.topk_weights, b.scatter, b.y, stream)
 
 
 def bf16_tensor_to_f32(t: torch.Tensor) -> np.ndarray:

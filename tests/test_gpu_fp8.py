@@ -1,0 +1,413 @@
+"""The FP8 operators on the GPU against the float64 oracle.
+
+Tolerances.  u = 2^-24.  Quantisation of bf16 is exact: codes and scales equal bit for bit.
+A product's sum over n runs is off by at most (n + 130) 2u times the sum of its terms'
+magnitudes (128 products within a run, n scaled sums).  bf16 output adds half a step, 2^-8
+of the value, and what the FP8 matrix instruction drops: each of 16 products is cut at 2^-13
+of the power of two of the largest, which is exact itself, so at most 15 2^-13 max <= 15 2^-13
+sum of magnitudes (fp8.MFMA_CUT).  On random data the cuts also average out: the 2-norm of
+the error stays under 2^-8 of the result's, what bf16's rounding alone may take.  The grouped FFN adds the steps of h's codes that its rounding can move
+(oracle.fp8.ffn_fp8's slack)."""
+from __future__ import annotations
+
+import sys
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import oracle
+from mxfp4_routed_expert_route_amd import inputs
+from oracle import fp8
+
+pytestmark = pytest.mark.gpu
+
+U24, BF16_HALF = 2.0 ** -24, 2.0 ** -8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from mxfp4_routed_expert_route_amd import binding
+    binding.load()
+
+
+def say(*a):
+    print("[fp8]", *a, file=sys.stderr, flush=True)
+
+
+def cuda(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def bf16_rows(rng, rows, K, spread=1.0):
+    v = rng.standard_normal((rows, K)) * np.exp(spread * rng.standard_normal((1, K)))
+    return inputs.f32_to_bf16_bits(v.astype(np.float32))
+
+
+def codes(rng, *shape):
+    c = rng.integers(0, 255, shape, dtype=np.int64)
+    return np.where(c >= 0x7F, c + 1, c).astype(np.uint8) & np.where(c == 254, 0xFE, 0xFF).astype(np.uint8)
+
+
+def scales(rng, *shape, size=1.0):
+    return (rng.uniform(0.5, 1.5, shape) * size).astype(np.float32)
+
+
+# ------------------------------------------------------------ quantisation
+
+def gpu_quantize(bits):
+    from mxfp4_routed_expert_route_amd import binding
+    rows, K = bits.shape
+    q = torch.full((rows, K), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.full((rows, -(-K // 128)), -7.0, device="cuda")
+    binding.moe_quantize_fp8(cuda(bits.view(np.int16)), q, s)
+    torch.cuda.synchronize()
+    return q.cpu().numpy(), s.cpu().numpy()
+
+
+@pytest.mark.parametrize("rows,K", [(1, 16), (1, 128), (3, 144), (5, 2064), (17, 4096), (300, 112), (1000, 1024),
+                                    (1, 65536), (33, 272)])
+def test_quantize_is_exact(rows, K):
+    say("quantize", rows, K)
+    rng = np.random.default_rng(rows + K)
+    bits = bf16_rows(rng, rows, K)
+    q, s = gpu_quantize(bits)
+    rq, rs = fp8.quantize_fp8(inputs.bf16_bits_to_f32(bits))
+    assert np.array_equal(q, rq) and np.array_equal(s, rs)
+
+
+def test_quantize_borders_and_extremes():
+    # every bf16 magnitude pattern as the run's largest value, beside values on or near code borders
+    rng = np.random.default_rng(3)
+    amax = np.arange(0, 0x7F80, 61, dtype=np.uint16)                     # 0, denormals .. just below infinity
+    bits = np.zeros((amax.size, 128), np.uint16)
+    bits[:, 5] = amax | 0x8000
+    for j in range(6, 128):
+        down = rng.integers(0, 1300, amax.size)
+        bits[:, j] = np.maximum(amax.astype(np.int64) - down, 0).astype(np.uint16) | (rng.integers(0, 2, amax.size) << 15).astype(np.uint16)
+    q, s = gpu_quantize(bits)
+    rq, rs = fp8.quantize_fp8(inputs.bf16_bits_to_f32(bits))
+    assert np.array_equal(s, rs)
+    assert np.array_equal(q, rq), np.argwhere(q != rq)[:5]
+    assert (fp8.decode_e4m3(q[amax > 0x1000, 5]) == -448).all()
+
+
+def test_quantize_zeros_infinities_and_nan():
+    bits = np.zeros((5, 256), np.uint16)
+    bits[1, 3] = 0x7F80
+    bits[2, 200] = 0xFF80
+    bits[3, 0] = 0x7FC1
+    bits[4, :] = 0x8000
+    bits[1:4, 100] = 0x3F80
+    q, s = gpu_quantize(bits)
+    rq, rs = fp8.quantize_fp8(inputs.bf16_bits_to_f32(bits))
+    assert np.array_equal(q, rq) and np.array_equal(s, rs, equal_nan=True)
+
+
+# ------------------------------------------------------------ dense product
+
+def gpu_gemm(xq, xs, w, ws, f32):
+    from mxfp4_routed_expert_route_amd import binding
+    M, N, K = xq.shape[0], w.shape[0], xq.shape[1]
+    y = torch.full((M + 1, N), -7.0, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    work = torch.full((binding.moe_gemm_fp8_workspace_bytes(M, N, K),), 0x7F, dtype=torch.uint8, device="cuda")
+    binding.moe_gemm_fp8(cuda(xq), cuda(xs), cuda(w), cuda(ws), y[:M], work)
+    torch.cuda.synchronize()
+    assert (y[M] == -7.0).all()        # nothing behind the last row
+    return y[:M].float().cpu().numpy().astype(np.float64)
+
+
+def gemm_close(y, xq, xs, w, ws, f32):
+    ref, mag = fp8.gemm_fp8(xq, xs, w, ws)
+    cut = 0.0 if f32 else fp8.MFMA_CUT * mag
+    bound = (xs.shape[1] + 130) * 2 * U24 * mag + cut + (0.0 if f32 else BF16_HALF * (np.abs(ref) + cut)) + 1e-37
+    bad = ~(np.abs(y - ref) <= bound)
+    assert y.size < 100 or np.linalg.norm(y - ref) <= BF16_HALF * np.linalg.norm(ref)
+    assert not bad.any(), (np.argwhere(bad)[:5], np.abs(y - ref).max())
+
+
+GEMM_SHAPES = [   # M, N, K
+    (1, 1, 16), (1, 256, 128), (2, 130, 144), (3, 17, 2064), (15, 255, 1024), (16, 128, 4096), (17, 300, 272),
+    (33, 64, 512), (64, 513, 640), (77, 1003, 2064), (100, 128, 112), (129, 257, 400), (200, 1024, 2048),
+    (257, 384, 1152), (300, 1000, 1040), (513, 640, 256), (600, 2049, 144), (1025, 520, 384), (1, 4096, 4096),
+    (9, 2048, 8192), (40, 96, 16384), (256, 256, 128), (2050, 256, 256),
+]
+
+
+@pytest.mark.parametrize("M,N,K", GEMM_SHAPES)
+@pytest.mark.parametrize("f32", [True, False])
+def test_gemm(M, N, K, f32):
+    say("gemm", M, N, K, f32)
+    rng = np.random.default_rng(M * 31 + N * 7 + K)
+    xq, w = codes(rng, M, K), codes(rng, N, K)
+    xs, ws = scales(rng, M, -(-K // 128)), scales(rng, -(-N // 128), -(-K // 128))
+    gemm_close(gpu_gemm(xq, xs, w, ws, f32), xq, xs, w, ws, f32)
+
+
+@pytest.mark.parametrize("M", [1, 20, 300])
+def test_gemm_scales_of_every_size_and_sign(M):
+    rng = np.random.default_rng(M)
+    N, K = 260, 656
+    xq, w = codes(rng, M, K), codes(rng, N, K)
+    xs = scales(rng, M, 6) * np.exp2(rng.integers(-40, 40, (M, 6))).astype(np.float32)
+    ws = scales(rng, 3, 6) * np.exp2(rng.integers(-40, 40, (3, 6))).astype(np.float32) * rng.choice([-1, 1], (3, 6)).astype(np.float32)
+    ws[1, 2] = 0.0
+    gemm_close(gpu_gemm(xq, xs, w, ws, True), xq, xs, w, ws, True)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 200, 272), (40, 200, 272), (300, 300, 272)])
+def test_gemm_nan_stays_in_its_row_and_column(M, N, K):
+    rng = np.random.default_rng(1)
+    xq, w = codes(rng, M, K), codes(rng, N, K)
+    xs, ws = scales(rng, M, 3), scales(rng, 2 if N <= 256 else 3, 3)
+    xq[M // 2, K - 1] = 0x7F
+    w[77, 3] = 0xFF
+    y = gpu_gemm(xq, xs, w, ws, True)
+    nan = np.zeros((M, N), bool)
+    nan[M // 2] = True
+    nan[:, 77] = True
+    assert np.array_equal(np.isnan(y), nan)
+    xq[M // 2, K - 1] = 0
+    w[77, 3] = 0
+    ref, mag = fp8.gemm_fp8(xq, xs, w, ws)
+    assert (np.abs(y - ref) <= (133 * 2 * U24 * mag) + 1e-37)[~nan].all()
+
+
+def test_gemm_offsets_past_32_bits():
+    # weights of 4.3 GiB and an output of 4.2 GiB: the last rows and columns are checked
+    from mxfp4_routed_expert_route_amd import binding
+    N, K = 70000, 65536
+    free, _ = torch.cuda.mem_get_info()
+    if free < 30 << 30:
+        pytest.skip("needs 30 GiB")
+    for M in (2, 32768):
+        if M == 2:
+            n, kk = N, K
+        else:
+            n, kk = 70000, 128
+        say("gemm", M, n, kk)
+        g = torch.Generator(device="cuda").manual_seed(M)
+        w = torch.randint(0, 120, (n, kk), dtype=torch.uint8, device="cuda", generator=g)
+        xq = torch.randint(0, 120, (M, kk), dtype=torch.uint8, device="cuda", generator=g)
+        xs = torch.rand(M, kk // 128, device="cuda", generator=g)
+        ws = torch.rand(-(-n // 128), kk // 128, device="cuda", generator=g)
+        y = torch.empty(M, n, dtype=torch.bfloat16, device="cuda")
+        work = torch.empty(binding.moe_gemm_fp8_workspace_bytes(M, n, kk), dtype=torch.uint8, device="cuda")
+        binding.moe_gemm_fp8(xq, xs, w, ws, y, work)
+        torch.cuda.synchronize()
+        rows, cols = slice(max(0, M - 3), M), slice(n - 130, n)
+        full = ws[(torch.arange(n, device="cuda") // 128)[cols]]
+        got = y[rows, cols].float().cpu().numpy()
+        ref, mag = fp8.gemm_fp8(xq[rows].cpu().numpy(), xs[rows].cpu().numpy(), np.zeros((0, kk), np.uint8), np.zeros((0, kk // 128)))
+        a = fp8.decode_e4m3(xq[rows].cpu().numpy()) * fp8.expand_rows(xs[rows].cpu().numpy(), kk)
+        b = fp8.decode_e4m3(w[cols].cpu().numpy()) * fp8.expand_rows(full.cpu().numpy(), kk)
+        ref, mag = a @ b.T, np.abs(a) @ np.abs(b).T
+        assert (np.abs(got - ref) <= ((kk // 128 + 130) * 2 * U24 + fp8.MFMA_CUT) * mag * 1.01 + BF16_HALF * np.abs(ref)).all()
+        del w, y, work
+        torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------ grouped FFN
+
+def ffn_inputs(rng, T, E, k, H, I, ids=None):
+    if ids is None:
+        ids = np.argsort(rng.standard_normal((T, E)), axis=1)[:, :k]
+    counts, offsets, gather, scatter = oracle.expert_offsets(ids, E)
+    return dict(x=bf16_rows(rng, T, H, 0.5), w1=codes(rng, E, 2 * I, H), w2=codes(rng, E, H, I),
+                w1s=scales(rng, E, 2 * I // 128, H // 128, size=1 / (64 * H ** 0.5)),
+                w2s=scales(rng, E, H // 128, I // 128, size=1 / (64 * I ** 0.5)), counts=counts, offsets=offsets,
+                gather=gather, scatter=scatter, k=k, ids=ids)
+
+
+def to_gpu(d):
+    return {n: cuda(v.view(np.int16) if n == "x" else v) for n, v in d.items() if isinstance(v, np.ndarray)}
+
+
+def gpu_ffn(d, limit, stream=None):
+    from mxfp4_routed_expert_route_amd import binding
+    T, H = d["x"].shape
+    E, I = d["w1"].shape[0], d["w1"].shape[1] // 2
+    t = to_gpu(d)
+    slots = d["gather"].size
+    y = torch.full((slots + 1, H), -7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((binding.moe_fp8_workspace_bytes(T, E, d["k"], H, I),), 0x7F, dtype=torch.uint8, device="cuda")
+    binding.moe_grouped_ffn_fp8(t["x"], d["k"], t["w1"], t["w1s"], t["w2"], t["w2s"], t["counts"], t["offsets"],
+                                t["gather"], limit, y[:slots], ws, stream)
+    torch.cuda.synchronize()
+    assert (y[slots] == -7.0).all()
+    return y[:slots].float().cpu().numpy().astype(np.float64)
+
+
+def ffn_close(y, d, limit, bf16=True):
+    ref, slack = fp8.ffn_fp8(inputs.bf16_bits_to_f32(d["x"]), d["gather"], d["offsets"], d["k"], d["w1"], d["w1s"],
+                             d["w2"], d["w2s"], limit)
+    bad = ~(np.abs(y - ref) <= slack + BF16_HALF * (np.abs(ref) + slack) + 1e-37)
+    assert not bad.any(), (np.argwhere(bad)[:5], np.abs(y - ref).max(), np.abs(ref).max())
+    # 2-norm: bf16's rounding, at most 2^-8; the cut moves a gate by about 1.4e-5, so one code of
+    # h in 2000 (a 16th of a step's 2^-3) by one step: sqrt(1 / 2000) / 8 < 2^-8 again
+    assert y.size < 1000 or np.linalg.norm(y - ref) <= 2 * BF16_HALF * np.linalg.norm(ref)
+
+
+FFN_SHAPES = [   # T, E, k, H, I
+    (1, 1, 1, 128, 128), (1, 8, 2, 256, 128), (3, 4, 4, 384, 256), (16, 256, 6, 256, 128), (17, 2, 1, 128, 384),
+    (40, 3, 2, 640, 256), (64, 8, 8, 256, 512), (100, 5, 2, 512, 384), (130, 2, 2, 256, 256), (257, 3, 1, 384, 128),
+    (300, 16, 6, 256, 256), (520, 4, 2, 128, 640), (8, 40, 6, 1024, 512), (700, 2, 2, 256, 128), (90, 1, 1, 2048, 256),
+    (1200, 9, 3, 128, 128), (30, 12, 1, 4096, 128),
+]
+
+
+@pytest.mark.parametrize("shape", FFN_SHAPES, ids=str)
+@pytest.mark.parametrize("limit", [10.0, 0.0])
+def test_ffn(shape, limit):
+    say("ffn", shape, limit)
+    d = ffn_inputs(np.random.default_rng(sum(shape)), *shape)
+    ffn_close(gpu_ffn(d, limit), d, limit)
+
+
+@pytest.mark.parametrize("T", [5, 70, 400, 1500])
+def test_ffn_skewed_and_empty_experts(T):
+    # expert 3 takes every token, most others none, the last one a single row
+    rng = np.random.default_rng(T)
+    E, k = 24, 2
+    ids = np.stack([np.full(T, 3), np.where(np.arange(T) % 5 == 0, 7, 11)], 1)
+    ids[-1, 1] = 23
+    d = ffn_inputs(rng, T, E, k, 256, 256, ids)
+    ffn_close(gpu_ffn(d, 2.0), d, 2.0)
+
+
+def test_ffn_saturated_gates():
+    rng = np.random.default_rng(8)
+    d = ffn_inputs(rng, 60, 4, 2, 256, 128)
+    d["w1s"] *= 40
+    ffn_close(gpu_ffn(d, 10.0), d, 10.0)
+    ffn_close(gpu_ffn(d, float("inf")), d, 0.0)
+
+
+def test_ffn_nan_token_stays_in_its_rows():
+    rng = np.random.default_rng(4)
+    for T in (6, 90, 500):
+        d = ffn_inputs(rng, T, 6, 3, 256, 128)
+        d["x"][T // 2, 17] = 0x7FC0
+        y = gpu_ffn(d, 10.0)
+        of = d["gather"] // 3 == T // 2
+        assert np.isnan(y[of]).all() and not np.isnan(y[~of]).any()
+
+
+def test_ffn_rows_past_the_last_expert_are_left():
+    # a plan that covers fewer rows than T*k (its counts say so): the rows behind stay
+    from mxfp4_routed_expert_route_amd import binding
+    for T, cut in ((20, 7), (400, 200)):
+        rng = np.random.default_rng(cut)
+        E, k, H, I = 3, 2, 256, 128
+        d = ffn_inputs(rng, T, E, k, H, I)
+        d["counts"][2] -= cut
+        d["offsets"][3] -= cut
+        t = to_gpu(d)
+        y = torch.full((T * k, H), -7.0, dtype=torch.bfloat16, device="cuda")
+        ws = torch.empty(binding.moe_fp8_workspace_bytes(T, E, k, H, I), dtype=torch.uint8, device="cuda")
+        binding.moe_grouped_ffn_fp8(t["x"], k, t["w1"], t["w1s"], t["w2"], t["w2s"], t["counts"], t["offsets"],
+                                    t["gather"], 10.0, y, ws)
+        torch.cuda.synchronize()
+        assert (y[-cut:] == -7.0).all()
+        got = y[:-cut].float().cpu().numpy().astype(np.float64)
+        full = ffn_inputs(np.random.default_rng(cut), T, E, k, H, I)
+        ref, slack = fp8.ffn_fp8(inputs.bf16_bits_to_f32(full["x"]), full["gather"], full["offsets"], k, full["w1"],
+                                 full["w1s"], full["w2"], full["w2s"], 10.0)
+        assert (np.abs(got - ref[:-cut]) <= (slack + BF16_HALF * (np.abs(ref) + slack) + 1e-37)[:-cut]).all()
+
+
+# ------------------------------------------------------------ a run of them together
+
+def test_layer_of_scored_routing_fp8_experts_and_a_shared_expert():
+    """Router product, scored routing, grouped FP8 FFN, combine; beside it a dense product."""
+    from mxfp4_routed_expert_route_amd import binding, layer
+    for T in (1, 30, 200):
+        say("layer", T)
+        rng = np.random.default_rng(T)
+        E, k, H, I = 16, 4, 512, 256
+        d = ffn_inputs(rng, T, E, k, H, I)
+        t = to_gpu(d)
+        router, router_s = codes(rng, E, H), scales(rng, 1, H // 128, size=1 / (64 * H ** 0.5))
+        xq = torch.empty(T, H, dtype=torch.float8_e4m3fn, device="cuda")
+        xs = torch.empty(T, H // 128, device="cuda")
+        logits = torch.empty(T, E, device="cuda")
+        binding.moe_quantize_fp8(t["x"], xq, xs)
+        binding.moe_gemm_fp8(xq, xs, cuda(router), cuda(router_s), logits)
+        bias = (rng.standard_normal(E) * 0.2).astype(np.float32)
+        b = layer.LayerBuffers.allocate_fp8(T, E, k, H, I)
+        dev = dict(logits=logits, x=t["x"], w1=t["w1"], w1_s=t["w1s"], w2=t["w2"], w2_s=t["w2s"])
+        layer.run_layer_fp8(dev, b, 10.0, score="sigmoid", bias=cuda(bias), groups=4, topk_groups=2, scale=2.5)
+        torch.cuda.synchronize()
+        rq, rs = fp8.quantize_fp8(inputs.bf16_bits_to_f32(d["x"]))
+        gemm_close(logits.cpu().numpy().astype(np.float64), rq, rs, router, router_s, True)
+        ids, w = fp8.route_scored(logits.cpu().numpy(), k, score="sigmoid", bias=bias, groups=4, topk_groups=2, scale=2.5)
+        assert np.array_equal(b.topk_ids.cpu().numpy(), ids)
+        _, offsets, gather, scatter = oracle.expert_offsets(ids, E)
+        ys, slack = fp8.ffn_fp8(inputs.bf16_bits_to_f32(d["x"]), gather, offsets, k, d["w1"], d["w1s"], d["w2"],
+                                d["w2s"], 10.0)
+        slack = slack + BF16_HALF * (np.abs(ys) + slack)
+        y = (w[:, :, None] * ys[scatter].reshape(T, k, H)).sum(1)
+        bound = (w[:, :, None] * (slack + 16 * U24 * np.abs(ys))[scatter].reshape(T, k, H)).sum(1)
+        got = b.y.float().cpu().numpy()
+        assert (np.abs(got - y) <= bound + BF16_HALF * (np.abs(y) + bound)).all()
+
+
+@pytest.mark.parametrize("T", [8, 100, 600])
+def test_graph_replay_and_other_stream_match_eager(T):
+    """The whole run captured and replayed, with eager work on other inputs between replays."""
+    from mxfp4_routed_expert_route_amd import layer
+    rng = np.random.default_rng(T)
+    E, k, H, I = 16, 4, 512, 256
+    t = to_gpu(ffn_inputs(rng, T, E, k, H, I))
+    logits = torch.randn(T, E, device="cuda")
+    dev = dict(logits=logits, x=t["x"], w1=t["w1"], w1_s=t["w1s"], w2=t["w2"], w2_s=t["w2s"])
+    other = dict(dev, logits=torch.randn(T, E, device="cuda"))
+    how = dict(score="softmax", renormalize=False)
+    b = layer.LayerBuffers.allocate_fp8(T, E, k, H, I)
+    layer.run_layer_fp8(dev, b, 10.0, **how)
+    torch.cuda.synchronize()
+    names = ("topk_ids", "topk_weights", "gather", "y_sorted", "y")
+    bits = lambda x: x.view(torch.int16) if x.dtype == torch.bfloat16 else x.view(torch.int32)
+    ref = {n: bits(getattr(b, n)).clone() for n in names}
+    side = torch.cuda.Stream()
+    b2 = layer.LayerBuffers.allocate_fp8(T, E, k, H, I)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer.run_layer_fp8(dev, b2, 10.0, **how)
+    layer.run_layer_fp8(other, b, 10.0, **how)          # at the same time, other buffers
+    torch.cuda.synchronize()
+    for n in names:
+        assert torch.equal(bits(getattr(b2, n)), ref[n]), n
+    g = torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=side):
+        layer.run_layer_fp8(dev, b, 10.0, **how)
+    torch.cuda.synchronize()
+    for rep in range(3):
+        for n in names:
+            bits(getattr(b, n)).fill_(-1)
+        layer.run_layer_fp8(other, b, 0.0, **how)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        for n in names:
+            assert torch.equal(bits(getattr(b, n)), ref[n]), (rep, n)
+
+
+def test_binding_refuses_wrong_shapes_on_the_gpu():
+    from mxfp4_routed_expert_route_amd import binding
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    q, s = torch.zeros(4, 256, dtype=torch.uint8, device="cuda"), torch.zeros(4, 2, device="cuda")
+    with pytest.raises(ValueError, match="shape"):
+        binding.moe_quantize_fp8(x, q, s[:, :1])
+    with pytest.raises(ValueError, match="contiguous"):
+        binding.moe_quantize_fp8(x.t().contiguous().t(), q, s)
+    with pytest.raises(ValueError, match="must be"):
+        binding.moe_quantize_fp8(x.half(), q, s)
+    with pytest.raises(ValueError, match="shape"):
+        binding.moe_gemm_fp8(q, s, q, s, x)
+    with pytest.raises(binding.MoeError):
+        binding.moe_quantize_fp8(x[:, :8].contiguous(), q[:, :8].contiguous(), s[:, :1].contiguous())
