@@ -85,8 +85,8 @@ size_t moe_gemm_fp8_workspace_bytes(int64_t M, int32_t N, int32_t K);
  *   y_sorted  bf16  [T*k][H]                 out; 16-byte aligned
  *   ws        workspace of at least moe_fp8_workspace_bytes(T, E, k, H, I) bytes,
  *             16-byte aligned; contents on entry are ignored.
- * H and I are multiples of 128, at most 65536, with H * I below 2^31 (one expert's W1
- * stays below 4 GiB); activations fit as for moe_grouped_ffn_mxfp4.  T = 0 enqueues
+ * H and I are multiples of 128, at most 65536, with H * I at most 2^31 - 2^20 (32-bit
+ * offsets within an expert's W1); activations fit as for moe_grouped_ffn_mxfp4.  T = 0 enqueues
  * nothing.  Rows of y_sorted behind the last expert's rows are left as they were.
  */
 moe_status moe_grouped_ffn_fp8(const uint16_t* x, int64_t T, int32_t H, int32_t I, int32_t E,

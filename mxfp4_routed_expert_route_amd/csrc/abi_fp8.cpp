@@ -56,7 +56,7 @@ moe_status moe_quantize_fp8(const uint16_t* x, int64_t rows, int32_t K, uint8_t*
                             void* stream) {
   const moe_status s = moe::check_quantize_fp8(x, rows, K, q, scale);
   if (s != MOE_OK || rows == 0) return s;
-  return from_hip(moe::launch_quantize_fp8(x, rows, K, q, scale, as_stream(stream)));
+  return from_hip(moe::launch_quantize_fp8(x, rows, K, q, scale, (K + 127) / 128, 1, as_stream(stream)));
 }
 
 moe_status moe_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, int32_t N, int32_t K,

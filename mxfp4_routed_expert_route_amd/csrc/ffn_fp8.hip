@@ -1,5 +1,7 @@
 // The grouped FFN over block-scaled FP8 weights and the dense product: dispatch.
 #include "fp8.h"
+#include "fp8_common.h"
+#include "fp8_plan.h"
 #include "validate_fp8.h"
 
 namespace moe {
@@ -19,7 +21,11 @@ hipError_t launch_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, i
   p.out_kind = f32 ? kFp8OutF32 : kFp8OutBf16;
   p.out = y;
   p.ld_out = N;
-  return launch_fp8_rows(p, stream);
+  p.act_rows = M;
+  p.scale_row = (K + kFp8Block - 1) / kFp8Block;
+  p.scale_k = 1;
+  const int tile_rows = fp8_gemm_tile_rows(M);
+  return tile_rows == 16 ? launch_fp8_rows(p, stream) : launch_fp8_tile(tile_rows, p, stream);
 }
 
 hipError_t launch_ffn_fp8(const uint16_t* x, int64_t T, int H, int I, int E, int k,
@@ -39,8 +45,10 @@ hipError_t launch_ffn_fp8(const uint16_t* x, int64_t T, int H, int I, int E, int
   hipError_t err = launch_plan(counts, offsets, E, L.tile_rows, slots, L.tile_bound, n_tiles, tiles,
                                stream);
   if (err != hipSuccess) return err;
-  err = launch_quantize_fp8(x, T, H, xq, xs, stream);
+  // scales of x and h are kept run by run, [K/128][rows]: a tile's are contiguous in a step
+  err = launch_quantize_fp8(x, T, H, xq, xs, 1, T, stream);
   if (err != hipSuccess) return err;
+  const bool tiled = L.tile_rows > 16;
 
   Fp8Product p{};
   p.rows = slots;
@@ -52,20 +60,28 @@ hipError_t launch_ffn_fp8(const uint16_t* x, int64_t T, int H, int I, int E, int
   p.clamp = limit > 0.f && limit <= 3.402823466e38f ? 1 : 0;   // finite and positive
   p.act = xq;
   p.act_scale = xs;
+  p.act_rows = T;
+  p.scale_row = 1;
+  p.scale_k = T;
   p.w = w1;
   p.w_scale = w1s;
   p.K = H;
   p.n = 2 * I;
   p.gather = gather;
   p.out_kind = kFp8OutSwiglu;
-  p.out = h;
+  p.out = tiled ? static_cast<void*>(hq) : h;
+  p.out_scale = hs;
   p.ld_out = I;
-  err = launch_fp8_rows(p, stream);
+  err = tiled ? launch_fp8_tile(L.tile_rows, p, stream) : launch_fp8_rows(p, stream);
   if (err != hipSuccess) return err;
-  err = launch_quantize_fp8_f32(h, slots, I, hq, hs, stream);
-  if (err != hipSuccess) return err;
+  if (!tiled) {
+    err = launch_quantize_fp8_f32(h, slots, I, hq, hs, 1, slots, stream);
+    if (err != hipSuccess) return err;
+  }
   p.act = hq;
   p.act_scale = hs;
+  p.act_rows = slots;
+  p.scale_k = slots;
   p.w = w2;
   p.w_scale = w2s;
   p.K = I;
@@ -74,7 +90,7 @@ hipError_t launch_ffn_fp8(const uint16_t* x, int64_t T, int H, int I, int E, int
   p.out_kind = kFp8OutBf16;
   p.out = y_sorted;
   p.ld_out = H;
-  return launch_fp8_rows(p, stream);
+  return tiled ? launch_fp8_tile(L.tile_rows, p, stream) : launch_fp8_rows(p, stream);
 }
 
 }  // namespace moe

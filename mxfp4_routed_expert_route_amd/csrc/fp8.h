@@ -7,16 +7,18 @@
 
 namespace moe {
 
+// The scale of row r, run b goes to scale[r * scale_row + b * scale_k].
 hipError_t launch_quantize_fp8(const uint16_t* x, int64_t rows, int K, uint8_t* q, float* scale,
-                               hipStream_t stream);
+                               int64_t scale_row, int64_t scale_k, hipStream_t stream);
 hipError_t launch_quantize_fp8_f32(const float* x, int64_t rows, int K, uint8_t* q, float* scale,
-                                   hipStream_t stream);
+                                   int64_t scale_row, int64_t scale_k, hipStream_t stream);
 
 // What a product's epilogue writes.
 enum Fp8Out : int {
   kFp8OutBf16 = 0,   // bf16 [rows][n]
   kFp8OutF32 = 1,    // fp32 [rows][n]
-  kFp8OutSwiglu = 2  // fp32 h [rows][n / 2] from the gate and up halves of n
+  kFp8OutSwiglu = 2  // h from the gate and up halves of n: fp32 [rows][n / 2] (rows kernel), or
+                     // E4M3 codes with scales [n / 256][rows] in out_scale (tile kernel)
 };
 
 // One product, dense or grouped.  Rows p of the activations (grouped: p in a tile of the
@@ -24,7 +26,8 @@ enum Fp8Out : int {
 // the tile's expert (dense: expert 0, rows 0 .. rows - 1).
 struct Fp8Product {
   const uint8_t* act;        // [.][K]
-  const float* act_scale;    // [.][ceil(K/128)]
+  const float* act_scale;    // of row r, run b at [r * scale_row + b * scale_k]
+  int64_t act_rows, scale_row, scale_k;
   const uint8_t* w;          // [E][n][K]
   const float* w_scale;      // [E][ceil(n/128)][ceil(K/128)]
   int K, n;
@@ -38,10 +41,12 @@ struct Fp8Product {
   int clamp;
   int out_kind;              // Fp8Out
   void* out;
+  float* out_scale;
   int ld_out;
 };
 
-hipError_t launch_fp8_rows(const Fp8Product& p, hipStream_t stream);
+hipError_t launch_fp8_rows(const Fp8Product& p, hipStream_t stream);            // 16-row tiles
+hipError_t launch_fp8_tile(int tile_rows, const Fp8Product& p, hipStream_t stream);   // fp8_tile.hip
 
 hipError_t launch_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, int N, int K,
                            const uint8_t* w, const float* w_scale, bool f32, void* y, void* ws,

@@ -87,7 +87,8 @@ __device__ __forceinline__ floatx4 mfma_e4m3(i32x8 a, i32x8 b) {
                                                   e4m3_to_bf16(b[2 * i], b[2 * i + 1]), d, 0, 0, 0);
     return d;
   } else {
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d, 0, 0, 0, 127, 0, 127);
+    // zero scale operands select the form without scales
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d, 0, 0, 0, 0, 0, 0);
   }
 }
 

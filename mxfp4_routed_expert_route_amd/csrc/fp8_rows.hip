@@ -42,7 +42,7 @@ __global__ __launch_bounds__(64 * kWaves) void rows_kernel(Fp8Product p, int n_g
   const int nb = (p.K + kFp8Block - 1) / kFp8Block;
   const int half = p.n / 2;
   const uint8_t* arow = p.act + (valid ? row : 0) * static_cast<int64_t>(p.K);
-  const float* ascale = p.act_scale + (valid ? row : 0) * static_cast<int64_t>(nb);
+  const float* ascale = p.act_scale + (valid ? row : 0) * p.scale_row;
   const int64_t e_rows = static_cast<int64_t>(expert) * p.n;
   const int n_blocks = (p.n + kFp8Block - 1) / kFp8Block;
   int n0[kFrag];
@@ -68,7 +68,7 @@ __global__ __launch_bounds__(64 * kWaves) void rows_kernel(Fp8Product p, int n_g
     const i32x4 b0 = valid && in0 ? *reinterpret_cast<const i32x4*>(arow + k0) : z;
     const i32x4 b1 = valid && in1 ? *reinterpret_cast<const i32x4*>(arow + k0 + 64) : z;
     const i32x8 b = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
-    const float xs = valid ? ascale[kb] : 0.f;
+    const float xs = valid ? ascale[kb * p.scale_k] : 0.f;
 #pragma unroll
     for (int f = 0; f < kFrag; ++f) {
       const i32x4 a0 = wvalid[f] && in0 ? *reinterpret_cast<const i32x4*>(wrow[f] + k0) : z;

@@ -27,10 +27,12 @@ __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
 template <class In>
 __global__ __launch_bounds__(256) void quantize_kernel(const In* __restrict__ x, int64_t runs, int K,
                                                        int nb, uint8_t* __restrict__ q,
-                                                       float* __restrict__ scale) {
+                                                       float* __restrict__ scale, int64_t scale_row,
+                                                       int64_t scale_k) {
   const int64_t run = static_cast<int64_t>(blockIdx.x) * 16 + (threadIdx.x >> 4);
   const int64_t row = run / nb;
-  const int col = static_cast<int>(run - row * nb) * kFp8Block + 8 * (threadIdx.x & 15);
+  const int64_t b = run - row * nb;
+  const int col = static_cast<int>(b) * kFp8Block + 8 * (threadIdx.x & 15);
   const bool here = run < runs && col < K;   // K is a multiple of 16: all eight or none
   float v[8];
 #pragma unroll
@@ -51,27 +53,28 @@ __global__ __launch_bounds__(256) void quantize_kernel(const In* __restrict__ x,
   if (!finite) o.x = o.y = kNanCodes;
   if (!here) return;
   *reinterpret_cast<uint2*>(q + row * K + col) = o;
-  if ((threadIdx.x & 15) == 0) scale[run] = finite ? s.scale : __uint_as_float(0x7FC00000u);
+  if ((threadIdx.x & 15) == 0) scale[row * scale_row + b * scale_k] = finite ? s.scale : __uint_as_float(0x7FC00000u);
 }
 
 template <class In>
-hipError_t launch(const In* x, int64_t rows, int K, uint8_t* q, float* scale, hipStream_t stream) {
+hipError_t launch(const In* x, int64_t rows, int K, uint8_t* q, float* scale, int64_t scale_row,
+                  int64_t scale_k, hipStream_t stream) {
   const int nb = (K + kFp8Block - 1) / kFp8Block;
   const int64_t runs = rows * nb;
   quantize_kernel<<<dim3(static_cast<unsigned>((runs + 15) / 16)), dim3(256), 0, stream>>>(
-      x, runs, K, nb, q, scale);
+      x, runs, K, nb, q, scale, scale_row, scale_k);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_quantize_fp8(const uint16_t* x, int64_t rows, int K, uint8_t* q, float* scale,
-                               hipStream_t stream) {
-  return launch(x, rows, K, q, scale, stream);
+                               int64_t scale_row, int64_t scale_k, hipStream_t stream) {
+  return launch(x, rows, K, q, scale, scale_row, scale_k, stream);
 }
 hipError_t launch_quantize_fp8_f32(const float* x, int64_t rows, int K, uint8_t* q, float* scale,
-                                   hipStream_t stream) {
-  return launch(x, rows, K, q, scale, stream);
+                                   int64_t scale_row, int64_t scale_k, hipStream_t stream) {
+  return launch(x, rows, K, q, scale, scale_row, scale_k, stream);
 }
 
 }  // namespace moe

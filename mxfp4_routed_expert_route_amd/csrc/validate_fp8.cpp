@@ -22,8 +22,9 @@ moe_status check_sizes(int64_t T, int32_t E, int32_t k) {
 moe_status check_dims(int64_t T, int32_t k, int32_t H, int32_t I) {
   if (H <= 0 || I <= 0) return MOE_ERR_INVALID_ARGUMENT;
   if (H % 128 != 0 || I % 128 != 0 || H > kMaxDim || I > kMaxDim) return MOE_ERR_UNSUPPORTED;
-  // an expert's W1 (2 I rows of H bytes) stays below 4 GiB
-  if (static_cast<int64_t>(H) * I >= (int64_t{1} << 31)) return MOE_ERR_UNSUPPORTED;
+  // an expert's W1 (2 I rows of H bytes) is addressed with 32-bit offsets, below
+  // kRsrcOutOfRange (0xFFF00000)
+  if (static_cast<int64_t>(H) * I > kFp8MaxExpert) return MOE_ERR_UNSUPPORTED;
   const int64_t lim = kMaxActivationBytes;
   if (T * H * 2 > lim || T * k * static_cast<int64_t>(I) * 2 > lim ||
       T * k * static_cast<int64_t>(H) * 2 > lim)
@@ -56,7 +57,7 @@ moe_status fp8_workspace_layout(int64_t T, int32_t E, int32_t k, int32_t H, int3
   L.xs = take(t * (H / 128) * sizeof(float));
   L.hq = take(slots * I);
   L.hs = take(slots * (I / 128) * sizeof(float));
-  L.h = take(slots * I * sizeof(float));
+  L.h = L.tile_rows == 16 ? take(slots * I * sizeof(float)) : 0;
   L.plan = take(256 + static_cast<size_t>(L.tile_bound) * sizeof(RowTile));
   L.total = end > routing.offsets_bytes ? end : routing.offsets_bytes;
   *out = L;
