@@ -1,7 +1,6 @@
 // The grouped FFN over block-scaled FP8 weights and the dense product: dispatch.
 #include "fp8.h"
 #include "fp8_common.h"
-#include "fp8_plan.h"
 #include "validate_fp8.h"
 
 namespace moe {
@@ -24,8 +23,9 @@ hipError_t launch_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, i
   p.act_rows = M;
   p.scale_row = (K + kFp8Block - 1) / kFp8Block;
   p.scale_k = 1;
-  const int tile_rows = fp8_gemm_tile_rows(M);
-  return tile_rows == 16 ? launch_fp8_rows(p, stream) : launch_fp8_tile(tile_rows, p, stream);
+  bool done = false;
+  const hipError_t err = launch_fp8_rows(p, stream, &done);
+  return done || err != hipSuccess ? err : launch_fp8_dense(p, stream);
 }
 
 hipError_t launch_ffn_fp8(const uint16_t* x, int64_t T, int H, int I, int E, int k,
@@ -38,7 +38,6 @@ hipError_t launch_ffn_fp8(const uint16_t* x, int64_t T, int H, int I, int E, int
   float* xs = reinterpret_cast<float*>(wsb + L.xs);
   uint8_t* hq = reinterpret_cast<uint8_t*>(wsb + L.hq);
   float* hs = reinterpret_cast<float*>(wsb + L.hs);
-  float* h = reinterpret_cast<float*>(wsb + L.h);
   int32_t* n_tiles = reinterpret_cast<int32_t*>(wsb + L.plan);
   RowTile* tiles = reinterpret_cast<RowTile*>(wsb + L.plan + 256);
   const int64_t slots = T * k;
@@ -48,7 +47,6 @@ hipError_t launch_ffn_fp8(const uint16_t* x, int64_t T, int H, int I, int E, int
   // scales of x and h are kept run by run, [K/128][rows]: a tile's are contiguous in a step
   err = launch_quantize_fp8(x, T, H, xq, xs, 1, T, stream);
   if (err != hipSuccess) return err;
-  const bool tiled = L.tile_rows > 16;
 
   Fp8Product p{};
   p.rows = slots;
@@ -69,15 +67,11 @@ hipError_t launch_ffn_fp8(const uint16_t* x, int64_t T, int H, int I, int E, int
   p.n = 2 * I;
   p.gather = gather;
   p.out_kind = kFp8OutSwiglu;
-  p.out = tiled ? static_cast<void*>(hq) : h;
+  p.out = hq;
   p.out_scale = hs;
   p.ld_out = I;
-  err = tiled ? launch_fp8_tile(L.tile_rows, p, stream) : launch_fp8_rows(p, stream);
+  err = launch_fp8_grouped(L.tile_rows, p, stream);
   if (err != hipSuccess) return err;
-  if (!tiled) {
-    err = launch_quantize_fp8_f32(h, slots, I, hq, hs, 1, slots, stream);
-    if (err != hipSuccess) return err;
-  }
   p.act = hq;
   p.act_scale = hs;
   p.act_rows = slots;
@@ -90,7 +84,7 @@ hipError_t launch_ffn_fp8(const uint16_t* x, int64_t T, int H, int I, int E, int
   p.out_kind = kFp8OutBf16;
   p.out = y_sorted;
   p.ld_out = H;
-  return tiled ? launch_fp8_tile(L.tile_rows, p, stream) : launch_fp8_rows(p, stream);
+  return launch_fp8_grouped(L.tile_rows, p, stream);
 }
 
 }  // namespace moe

@@ -3,22 +3,20 @@
 #include <hip/hip_runtime.h>
 #include <cstdint>
 
-#include "config.h"
+#include "fp8_plan.h"
 
 namespace moe {
 
 // The scale of row r, run b goes to scale[r * scale_row + b * scale_k].
 hipError_t launch_quantize_fp8(const uint16_t* x, int64_t rows, int K, uint8_t* q, float* scale,
                                int64_t scale_row, int64_t scale_k, hipStream_t stream);
-hipError_t launch_quantize_fp8_f32(const float* x, int64_t rows, int K, uint8_t* q, float* scale,
-                                   int64_t scale_row, int64_t scale_k, hipStream_t stream);
 
 // What a product's epilogue writes.
 enum Fp8Out : int {
   kFp8OutBf16 = 0,   // bf16 [rows][n]
   kFp8OutF32 = 1,    // fp32 [rows][n]
-  kFp8OutSwiglu = 2  // h from the gate and up halves of n: fp32 [rows][n / 2] (rows kernel), or
-                     // E4M3 codes with scales [n / 256][rows] in out_scale (tile kernel)
+  kFp8OutSwiglu = 2  // h from the gate and up halves of n: E4M3 codes [rows][n / 2], with scales
+                     // [n / 256][rows] in out_scale (grouped only)
 };
 
 // One product, dense or grouped.  Rows p of the activations (grouped: p in a tile of the
@@ -45,8 +43,11 @@ struct Fp8Product {
   int ld_out;
 };
 
-hipError_t launch_fp8_rows(const Fp8Product& p, hipStream_t stream);            // 16-row tiles
-hipError_t launch_fp8_tile(int tile_rows, const Fp8Product& p, hipStream_t stream);   // fp8_tile.hip
+// Dense, few tiles (fp8_rows.hip): sets *done, or leaves larger outputs to launch_fp8_dense.
+hipError_t launch_fp8_rows(const Fp8Product& p, hipStream_t stream, bool* done);
+// LDS tiles (fp8_tile.hip).  tile_rows: as the plan was cut (fp8_tile_rows).
+hipError_t launch_fp8_dense(const Fp8Product& p, hipStream_t stream);
+hipError_t launch_fp8_grouped(int tile_rows, const Fp8Product& p, hipStream_t stream);
 
 hipError_t launch_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, int N, int K,
                            const uint8_t* w, const float* w_scale, bool f32, void* y, void* ws,

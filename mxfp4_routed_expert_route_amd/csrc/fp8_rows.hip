@@ -1,124 +1,185 @@
-// Block-scaled FP8 product for few rows: tiles of up to 16 activation rows.
+// Dense block-scaled FP8 product on small tiles, K shared out among a workgroup's wavefronts.
 //
-// A workgroup takes one tile and 16 weight rows (SwiGLU: 16 gate rows and their 16 up
-// rows); its wavefronts share out the 128-element runs of K, each adds up scale * partial
-// product in fp32 over its runs, and the partial sums are added in wavefront order in LDS.
-// The weights are the MFMA's A operand and go straight to registers, 16 rows x 64
-// contiguous bytes per load.
+// A workgroup takes 16 MS activation rows x 16 NF weight rows.  Wavefront w takes the
+// 128-element runs w, w + W, ... of K, straight to registers and kDepth runs ahead, adds up
+// multiplier * partial product in fp32, and the W sums are added in wavefront order through
+// LDS.  A load takes 16 rows x 64 contiguous bytes, the operand's own shape.
+//
+// For outputs of few tiles, which are bound by latency: the LDS-tiled kernel takes about
+// 0.5 us a run of K however little a workgroup has to do, this one runs W of them at a time
+// and meets no barrier before the end.  Measured (us in a graph, N = K = 4096, the tile that
+// the rule below takes / the 64 x 128 LDS tile): 1 row 5.8 / 17.1, 16 rows 7.5 / 17.5, 32
+// rows 10.3 / 20.2, 64 rows 12.4 / 22.5, 128 rows 16.0 / 23.1; a smaller tile than the rule's
+// reads the operands more often (16 x 16 tiles, 128 rows: 37.9), a larger one leaves CUs idle
+// (32 x 64 tiles, 16 rows: 14.0).  A single row of N = K = 4096 takes 5.2 us by the kernel
+// trace, of which its 16.8 MB of weights need 2.5.
 #include "fp8.h"
 #include "fp8_common.h"
 
 namespace moe {
 namespace {
 
-constexpr int kWaves = 4;
-
-template <int kOut>
-__global__ __launch_bounds__(64 * kWaves) void rows_kernel(Fp8Product p, int n_groups) {
-  constexpr bool kSwiglu = kOut == kFp8OutSwiglu;
-  constexpr int kFrag = kSwiglu ? 2 : 1;
-  __shared__ floatx4 part[kWaves][kFrag][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+template <int MS, int NF, int W, int kDepth, int kOut>
+__global__ __launch_bounds__(64 * W) void rows_kernel(Fp8Product p, int col_blocks) {
+  constexpr bool kFull = kOut == kFp8OutF32;
+  constexpr int TM = 16 * MS, cols = 16 * NF;
+  extern __shared__ __attribute__((aligned(16))) unsigned char rows_lds[];
+  floatx4* part = reinterpret_cast<floatx4*>(rows_lds);            // [W][MS][NF][64]
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int64_t tile = blockIdx.x / n_groups;
-  const int ng = static_cast<int>(blockIdx.x - tile * n_groups);
-  int expert = 0;
-  int64_t p_begin = tile * 16, p_end = p_begin + 16 < p.rows ? p_begin + 16 : p.rows;
-  if (p.tiles != nullptr) {
-    if (tile >= *p.n_tiles) return;   // uniform
-    const RowTile rt = p.tiles[tile];
-    expert = rt.expert;
-    p_begin = rt.p_begin;
-    p_end = rt.p_end;
+  const int tile = blockIdx.x / col_blocks;
+  const int n0 = (blockIdx.x - tile * col_blocks) * cols;
+  const int64_t p_begin = static_cast<int64_t>(tile) * TM, left = p.rows - p_begin;
+  const int rows = left < TM ? static_cast<int>(left) : TM;
+  const int K = p.K, nk = (K + kFp8Block - 1) / kFp8Block;
+  const int n_blk = (p.n + kFp8Block - 1) / kFp8Block;
+
+  // weights and activations: a resource on this tile's rows
+  const int w_rows = p.n - n0 < cols ? p.n - n0 : cols;
+  const __amdgpu_buffer_rsrc_t wrs = make_rsrc(p.w + static_cast<int64_t>(n0) * K,
+                                               static_cast<uint32_t>(w_rows) * static_cast<uint32_t>(K));
+  const __amdgpu_buffer_rsrc_t ars = make_rsrc(p.act + p_begin * K,
+                                               static_cast<uint32_t>(rows) * static_cast<uint32_t>(K));
+  uint32_t woff[NF], aoff[MS];
+  const float* wscale[NF];
+  const float* ascale[MS];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) {
+    const int n = 16 * f + r16, b = (n0 + 16 * f) / kFp8Block;
+    woff[f] = n < w_rows ? static_cast<uint32_t>(n) * static_cast<uint32_t>(K) + 16u * g : kRsrcOutOfRange;
+    wscale[f] = p.w_scale + static_cast<int64_t>(b < n_blk ? b : n_blk - 1) * nk;   // past n: any
   }
-  // this lane's activation row
-  int64_t row = p_begin + r16;
-  bool valid = row < p_end;
-  if (valid && p.gather != nullptr) {
-    const int slot = p.gather[row];
-    valid = slot >= 0 && slot < p.rows;
-    row = valid ? slot / p.k_top : 0;
+#pragma unroll
+  for (int m = 0; m < MS; ++m) {
+    const int r = 16 * m + r16;
+    aoff[m] = r < rows ? static_cast<uint32_t>(r) * static_cast<uint32_t>(K) + 16u * g : kRsrcOutOfRange;
+    ascale[m] = p.act_scale + (p_begin + (r < rows ? r : 0)) * p.scale_row;
   }
-  const int nb = (p.K + kFp8Block - 1) / kFp8Block;
-  const int half = p.n / 2;
-  const uint8_t* arow = p.act + (valid ? row : 0) * static_cast<int64_t>(p.K);
-  const float* ascale = p.act_scale + (valid ? row : 0) * p.scale_row;
-  const int64_t e_rows = static_cast<int64_t>(expert) * p.n;
-  const int n_blocks = (p.n + kFp8Block - 1) / kFp8Block;
-  int n0[kFrag];
-  const uint8_t* wrow[kFrag];
-  const float* wscale[kFrag];
-  bool wvalid[kFrag];
+
+  struct Run {
+    i32x8 a[NF], b[MS];
+    float x[MS], w[NF];
+  };
+  auto load = [&](Run& r, int kb) {
+    const int k0 = kb * kFp8Block;
+    // past K (a short last run): zeros
+    const bool in0 = k0 + 16 * g < K, in1 = k0 + 64 + 16 * g < K;
 #pragma unroll
-  for (int f = 0; f < kFrag; ++f) {
-    n0[f] = ng * 16 + f * half;
-    const int n = n0[f] + r16;
-    wvalid[f] = n < p.n;
-    wrow[f] = p.w + (e_rows + (wvalid[f] ? n : 0)) * p.K;
-    wscale[f] = p.w_scale + (static_cast<int64_t>(expert) * n_blocks + n0[f] / kFp8Block) * nb;
-  }
-  floatx4 acc[kFrag];
+    for (int f = 0; f < NF; ++f) {
+      const i32x4 lo = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+          wrs, in0 ? woff[f] + k0 : kRsrcOutOfRange, 0, 0));
+      const i32x4 hi = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+          wrs, in1 ? woff[f] + k0 + 64 : kRsrcOutOfRange, 0, 0));
+      r.a[f] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
 #pragma unroll
-  for (int f = 0; f < kFrag; ++f) acc[f] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-  for (int kb = wave; kb < nb; kb += kWaves) {
-    const int k0 = kb * kFp8Block + 16 * g;   // lane group g: elements 16g.. and 64 + 16g..
-    const bool in0 = k0 < p.K, in1 = k0 + 64 < p.K;
-    const i32x4 z = {0, 0, 0, 0};
-    const i32x4 b0 = valid && in0 ? *reinterpret_cast<const i32x4*>(arow + k0) : z;
-    const i32x4 b1 = valid && in1 ? *reinterpret_cast<const i32x4*>(arow + k0 + 64) : z;
-    const i32x8 b = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
-    const float xs = valid ? ascale[kb * p.scale_k] : 0.f;
+    for (int m = 0; m < MS; ++m) {
+      const i32x4 lo = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+          ars, in0 ? aoff[m] + k0 : kRsrcOutOfRange, 0, 0));
+      const i32x4 hi = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(
+          ars, in1 ? aoff[m] + k0 + 64 : kRsrcOutOfRange, 0, 0));
+      r.b[m] = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
 #pragma unroll
-    for (int f = 0; f < kFrag; ++f) {
-      const i32x4 a0 = wvalid[f] && in0 ? *reinterpret_cast<const i32x4*>(wrow[f] + k0) : z;
-      const i32x4 a1 = wvalid[f] && in1 ? *reinterpret_cast<const i32x4*>(wrow[f] + k0 + 64) : z;
-      const i32x8 a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
-      const floatx4 d = mfma_e4m3<kOut == kFp8OutF32>(a, b);
-      const float s = xs * wscale[f][kb];
+    for (int m = 0; m < MS; ++m) r.x[m] = ascale[m][kb];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[f][i] = fmaf(d[i], s, acc[f][i]);
+    for (int f = 0; f < NF; ++f) r.w[f] = wscale[f][kb];
+  };
+  floatx4 acc[MS][NF];
+#pragma unroll
+  for (int m = 0; m < MS; ++m)
+#pragma unroll
+    for (int f = 0; f < NF; ++f) acc[m][f] = floatx4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const Run& r) {
+#pragma unroll
+    for (int m = 0; m < MS; ++m)
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        const floatx4 d = mfma_e4m3<kFull>(r.a[f], r.b[m]);
+        const float s = r.x[m] * r.w[f];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][f][i] = fmaf(d[i], s, acc[m][f][i]);
+      }
+  };
+  Run ring[kDepth];
+#pragma unroll
+  for (int d = 0; d < kDepth; ++d)
+    if (wave + d * W < nk) load(ring[d], wave + d * W);   // uniform
+  for (int kb = wave; kb < nk; kb += kDepth * W) {
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      if (kb + d * W < nk) multiply(ring[d]);
+      if (kb + (kDepth + d) * W < nk) load(ring[d], kb + (kDepth + d) * W);
     }
   }
 #pragma unroll
-  for (int f = 0; f < kFrag; ++f) part[wave][f][lane] = acc[f];
+  for (int m = 0; m < MS; ++m)
+#pragma unroll
+    for (int f = 0; f < NF; ++f) part[((wave * MS + m) * NF + f) * 64 + lane] = acc[m][f];
   __syncthreads();
-  if (wave != 0) return;
-  floatx4 sum[kFrag];
+
+  // the fragments' sums are shared out among the wavefronts
+  for (int u = wave; u < MS * NF; u += W) {
+    const int m = u / NF, f = u - m * NF;
+    floatx4 s = part[u * 64 + lane];
 #pragma unroll
-  for (int f = 0; f < kFrag; ++f) {
-    sum[f] = part[0][f][lane];
-    for (int w = 1; w < kWaves; ++w) sum[f] += part[w][f][lane];
+    for (int w = 1; w < W; ++w) s += part[(w * MS * NF + u) * 64 + lane];
+    if (16 * m + r16 >= rows) continue;
+    const int c = n0 + 16 * f + 4 * g;
+    const int64_t at = (p_begin + 16 * m + r16) * p.ld_out + c;
+    const bool wide = p.n % 4 == 0;   // columns come in whole fours, on 8 or 16 bytes
+    if constexpr (kOut == kFp8OutF32) {
+      float* dst = static_cast<float*>(p.out) + at;
+      if (wide && c < p.n) {
+        *reinterpret_cast<floatx4*>(dst) = s;
+      } else {
+        for (int i = 0; i < 4; ++i)
+          if (c + i < p.n) dst[i] = s[i];
+      }
+    } else {
+      uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
+      if (wide && c < p.n) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3]));
+      } else {
+        for (int i = 0; i < 4; ++i)
+          if (c + i < p.n) dst[i] = f32_to_bf16_bits(s[i]);
+      }
+    }
   }
-  if (p_begin + r16 >= p_end) return;
-  const int64_t out_row = (p_begin + r16) * p.ld_out;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = ng * 16 + 4 * g + i;
-    if (n >= (kSwiglu ? half : p.n)) break;
-    if constexpr (kSwiglu)
-      static_cast<float*>(p.out)[out_row + n] = swiglu_fp8(sum[0][i], sum[1][i], p.limit, p.clamp != 0);
-    else if constexpr (kOut == kFp8OutF32)
-      static_cast<float*>(p.out)[out_row + n] = sum[0][i];
-    else
-      static_cast<uint16_t*>(p.out)[out_row + n] = f32_to_bf16_bits(sum[0][i]);
-  }
+}
+
+template <int MS, int NF, int W, int kDepth, int kOut>
+hipError_t launch(const Fp8Product& p, hipStream_t stream) {
+  constexpr int lds = W * MS * NF * 64 * 16;
+  static_assert(lds <= 64 * 1024, "no attribute needed");
+  const int col_blocks = (p.n + 16 * NF - 1) / (16 * NF);
+  const int64_t tiles = (p.rows + 16 * MS - 1) / (16 * MS);
+  rows_kernel<MS, NF, W, kDepth, kOut>
+      <<<dim3(static_cast<unsigned>(tiles * col_blocks)), dim3(64 * W), lds, stream>>>(p, col_blocks);
+  return hipGetLastError();
+}
+
+// The smallest tile of which the output has at most one per CU; nothing for larger outputs.
+template <int kOut>
+hipError_t launch_fitting(const Fp8Product& p, hipStream_t stream, bool* done) {
+  *done = true;
+  auto fits = [&](int tm, int tn) {
+    return (p.rows + tm - 1) / tm * ((p.n + tn - 1) / tn) <= kFp8Cus;
+  };
+  if (fits(16, 16)) return launch<1, 1, 8, 2, kOut>(p, stream);
+  if (fits(32, 16)) return launch<2, 1, 8, 2, kOut>(p, stream);
+  if (fits(32, 32)) return launch<2, 2, 8, 2, kOut>(p, stream);
+  if (fits(32, 64)) return launch<2, 4, 8, 1, kOut>(p, stream);
+  *done = false;
+  return hipSuccess;
 }
 
 }  // namespace
 
-hipError_t launch_fp8_rows(const Fp8Product& p, hipStream_t stream) {
-  const int cols = p.out_kind == kFp8OutSwiglu ? p.n / 2 : p.n;
-  const int n_groups = (cols + 15) / 16;
-  const int64_t tiles = p.tiles ? p.tile_bound : (p.rows + 15) / 16;
-  const dim3 grid(static_cast<unsigned>(tiles * n_groups)), block(64 * kWaves);
-  if (p.out_kind == kFp8OutSwiglu)
-    rows_kernel<kFp8OutSwiglu><<<grid, block, 0, stream>>>(p, n_groups);
-  else if (p.out_kind == kFp8OutF32)
-    rows_kernel<kFp8OutF32><<<grid, block, 0, stream>>>(p, n_groups);
-  else
-    rows_kernel<kFp8OutBf16><<<grid, block, 0, stream>>>(p, n_groups);
-  return hipGetLastError();
+hipError_t launch_fp8_rows(const Fp8Product& p, hipStream_t stream, bool* done) {
+  return p.out_kind == kFp8OutF32 ? launch_fitting<kFp8OutF32>(p, stream, done)
+                                  : launch_fitting<kFp8OutBf16>(p, stream, done);
 }
 
 }  // namespace moe

@@ -38,9 +38,14 @@ __device__ __forceinline__ i32x4 lds_rsrc(const void* base, uint32_t bytes) {
 // voff past the resource give zeros.  In assembly so that the compiler, which cannot tell
 // the stages apart, does not wait for all copies before every LDS read; wait_copies counts
 // them.  They write no register.
+template <bool kNt = false>   // kNt: non-temporal
 __device__ __forceinline__ void copy16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-               :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
+  if constexpr (kNt)
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
 }
 __device__ __forceinline__ void copy4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
@@ -61,305 +66,481 @@ __device__ __forceinline__ void barrier() {
   asm volatile("" ::: "memory");
 }
 
+// Non-temporal: with ordinary stores, the second product of 12,288 rows x 4096 columns (100 MB
+// out, 2.1 GB of weights in) takes 436 us, with these 406.
+__device__ __forceinline__ void store16(void* p, i32x4 v) {
+  __builtin_nontemporal_store(v, static_cast<i32x4*>(p));
+}
+
 typedef __attribute__((address_space(4))) const float const_float;
+typedef __attribute__((address_space(4))) const int const_int;
 
 constexpr int kXcds = 8;
 
-template <int TM_, int TN_, int WM_, int WN_, int ST_>
+// kNt: weights are read non-temporally (shapes whose weights are read about once).
+template <int TM_, int TN_, int WM_, int WN_, int SW_, int SA_, bool Nt_>
 struct Shape {
-  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, ST = ST_;
+  static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
+  static constexpr int SW = SW_, SA = SA_;               // steps of weights / of activations in LDS
+  static constexpr bool Nt = Nt_;
   static constexpr int NW = WM * WN, threads = 64 * NW;
   static constexpr int MT = TM / WM / 16, NF = TN / WN / 16;
-  static constexpr int copies_w = TN / 8 / NW;                       // per wavefront and step
-  static constexpr int copies_a = TM / 8 >= NW ? TM / 8 / NW : 1;
-  static constexpr int copies = copies_w + copies_a + 1;
-  static constexpr int w_bytes = TN * 128, a_bytes = TM * 128, s_bytes = NW * 256;
-  static constexpr int stage = w_bytes + a_bytes + s_bytes;
-  static constexpr int lds = ST * stage;
-  static_assert(TN % (8 * NW) == 0 && NW % 2 == 0 && TM <= 64 * NW && lds <= 160 * 1024, "shape");
+  // copies a wavefront issues in a step: scales, activations, weights, in this order
+  static constexpr int copies_w = TN / 8 / NW;
+  static constexpr int copies_a = (TM / 8 + NW - 1) / NW;
+  static constexpr int copies = 1 + copies_a + copies_w;
+  // copies that may be on their way when a step begins: the weights are SW - 1 steps ahead, the
+  // activations SA - 1
+  static constexpr int on_way = (SA - 2) * copies + (SW > SA ? copies_w : 0);
+  static constexpr int w_bytes = TN * 128, a_bytes = TM * 128, s_bytes = (TM + 63) / 64 * 256;
+  static constexpr int a_at = SW * w_bytes, s_at = a_at + SA * a_bytes;
+  static constexpr int red_at = s_at + SA * s_bytes;     // [WN][TM] magnitudes of h's runs
+  static constexpr int slots_at = red_at + WN * TM * 4;  // gather entries of the next tile
+  static constexpr int dump_at = slots_at + s_bytes;     // where copies without rows write zeros
+  static constexpr int h_at = dump_at + 1024;            // [TM][128] codes of h
+  static constexpr int lds = h_at + (Nt ? TM * 128 : 0);
+  static constexpr int per_cu = 160 * 1024 / lds;        // workgroups of a CU
+  static_assert(TN % (8 * NW) == 0 && NW % 2 == 0 && TM <= 64 * NW && per_cu >= 1, "shape");
+  static_assert(SA >= 2 && (SW == SA || SW == SA + 1), "order of the copies");
 };
 
+// Workgroups go through (row tile, column block) pairs; the copies run some steps ahead of the
+// products and across pairs, so the next pair's first steps are on their way while this
+// one's results are written.
 template <class S, int kOut>
-__global__ __launch_bounds__(S::threads, S::NW == 8 ? 2 : (2 * S::lds <= 160 * 1024 ? 2 : 1))
-void tile_kernel(Fp8Product p, int col_blocks, int64_t n_work) {
+__global__ __launch_bounds__(S::threads, S::NW / 4 * S::per_cu)
+void tile_kernel(Fp8Product p, int col_blocks) {
   constexpr bool kSwiglu = kOut == kFp8OutSwiglu, kFull = kOut == kFp8OutF32;
   constexpr int MT = S::MT, NF = S::NF, NR = 16 * NF;
+  // Steps the copies are ahead.  Streaming shapes fill a step's LDS as soon as its barrier says it
+  // has been read; the others a little later, spread over the next step's fragments.
+  constexpr int kLate = S::Nt ? 0 : 1, kW = S::SW - kLate, kA = S::SA - kLate;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int wm = wave / S::WN, wn = wave % S::WN;
-
-  // consecutive workgroups go to the XCDs in turn: XCD x takes row tiles x, x + 8, ...,
-  // all column blocks of one from one L2
-  const int64_t xcd = blockIdx.x % kXcds, local = blockIdx.x / kXcds;
-  const int64_t tile = (local / col_blocks) * kXcds + xcd;
-  const int nb_col = static_cast<int>(local % col_blocks);
-  int expert = 0, rows;
-  int64_t p_begin;
-  if (p.tiles != nullptr) {
-    if (tile >= *p.n_tiles) return;   // uniform
-    const RowTile rt = p.tiles[tile];
-    expert = __builtin_amdgcn_readfirstlane(rt.expert);
-    p_begin = __builtin_amdgcn_readfirstlane(rt.p_begin);
-    rows = __builtin_amdgcn_readfirstlane(rt.p_end) - static_cast<int>(p_begin);
-  } else {
-    p_begin = tile * S::TM;
-    if (p_begin >= p.rows) return;
-    rows = p.rows - p_begin < S::TM ? static_cast<int>(p.rows - p_begin) : S::TM;
-  }
   const int K = p.K, nk = (K + kFp8Block - 1) / kFp8Block;
+  // steps past nk copy zeros; SwiGLU's next gather entries need some steps to arrive
+  constexpr int kLeast = kSwiglu ? 2 * kW : kW;
+  const int steps = nk < kLeast ? kLeast : nk;
   const int half = p.n / 2;
-  const int n0 = nb_col * (kSwiglu ? S::TN / 2 : S::TN);   // first output column
+  const int n_blk = (p.n + kFp8Block - 1) / kFp8Block;
+  const bool grouped = p.tiles != nullptr;
+  const int n_tiles = grouped ? *(const_int*)p.n_tiles : static_cast<int>((p.rows + S::TM - 1) / S::TM);
+
+  // Consecutive workgroups go to the XCDs in turn: XCD x takes row tiles x, x + 8, ..., all
+  // column blocks of one from one L2; its workgroups share out the pairs in turn.
+  const int xcd = blockIdx.x % kXcds;
+  const int stride = gridDim.x / kXcds;
+  struct Pair {
+    int tile, p_begin, expert, rows, n0;   // n0: first output column
+    int first;                             // first run of K it takes
+  };
+  auto pair_at = [&](int local) {
+    Pair w;
+    w.tile = (local / col_blocks) * kXcds + xcd;
+    w.n0 = local % col_blocks * (kSwiglu ? S::TN / 2 : S::TN);
+    w.first = S::Nt ? local % col_blocks * nk / col_blocks : 0;
+    w.expert = 0;
+    w.rows = 0;
+    w.p_begin = 0;
+    if (w.tile >= n_tiles) return w;
+    if (grouped) {
+      const_int* rt = (const_int*)(p.tiles + w.tile);   // expert, p_begin, p_end
+      w.expert = rt[0];
+      w.p_begin = rt[1];
+      w.rows = rt[2] - rt[1];
+    } else {
+      w.p_begin = w.tile * S::TM;
+      const int left = static_cast<int>(p.rows) - w.p_begin;
+      w.rows = left < S::TM ? left : S::TM;
+    }
+    return w;
+  };
+  int local = blockIdx.x / kXcds;
+  Pair cur = pair_at(local);
+  if (cur.tile >= n_tiles) return;   // uniform
 
   // ---- copies: this lane's place in a copy's 8 rows x 128 bytes, and the piece it fetches
   const int c_row = lane >> 3;                                    // copy j: LDS row 8 j + c_row
   const uint32_t c_piece = 16u * ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));   // j % 2 = wave % 2
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) unsigned char*)tile_lds));
-  // weights: a resource on the expert's slab (SwiGLU) or on this column block's rows
-  const uint8_t* wbase = p.w + (static_cast<int64_t>(expert) * p.n + (kSwiglu ? 0 : n0)) * K;
-  const int w_rows = kSwiglu ? p.n : (p.n - n0 < S::TN ? p.n - n0 : S::TN);
-  const i32x4 wrs = lds_rsrc(wbase, static_cast<uint32_t>(static_cast<int64_t>(w_rows) * K));
-  uint32_t woff[S::copies_w];
+  // weight row, from the column block's first, of an LDS row: fragment r / 16 % NF of wn = r / NR
+  auto weight_row = [&](int r) {
+    const int m = r & 15, f = (r >> 4) % NF, v = r / NR;
+    if (!kSwiglu) return v * NR + (f >> 1) * 32 + (m >> 2) * 8 + (f & 1) * 4 + (m & 3);
+    const int i = v * (NR / 2) + (m >> 2) * (2 * NF) + (f % (NF / 2)) * 4 + (m & 3);
+    return f < NF / 2 ? i : half + i;
+  };
+  // a wavefront's copies are 8 NW LDS rows apart, whose weight rows are the same number of rows
+  // apart for every lane: a scalar offset
+  static_assert((S::NW / 2) % NF == 0 || NF % (S::NW / 2) == 0, "uniform distance of copies");
+  const uint32_t woff = static_cast<uint32_t>(weight_row(8 * wave + c_row)) * static_cast<uint32_t>(K) + c_piece;
+  i32x4 wrs, ars, srs;
+  int w_rows, wk_first, ak_first;
+  uint32_t aoff[S::copies_a], soff;
+  const int* next_slots = reinterpret_cast<const int*>(tile_lds + S::slots_at);
+  auto aim_w = [&](const Pair& w) {
+    // weights: a resource from the column block's first row on, to the expert's last (SwiGLU) or
+    // the block's last
+    const uint8_t* wbase = p.w + (static_cast<int64_t>(w.expert) * p.n + w.n0) * K;
+    w_rows = kSwiglu ? p.n - w.n0 : (p.n - w.n0 < S::TN ? p.n - w.n0 : S::TN);
+    wrs = lds_rsrc(wbase, static_cast<uint32_t>(static_cast<int64_t>(w_rows) * K));
+    wk_first = w.first;
+  };
+  // its gather entries: read here (first pair) or from LDS
+  auto aim_a = [&](const Pair& w, auto first) {
+    ak_first = w.first;
+    // activations and their scales: dense, a resource on the tile's rows; grouped, on all
+    const int64_t a_first = grouped ? 0 : w.p_begin;
+    const int64_t a_count = grouped ? p.act_rows : static_cast<int64_t>(w.rows);
+    ars = lds_rsrc(p.act + a_first * K, static_cast<uint32_t>(a_count * K));
+    srs = lds_rsrc(p.act_scale + a_first * p.scale_row,
+                   static_cast<uint32_t>(4 * ((a_count - 1) * p.scale_row + (nk - 1) * p.scale_k + 1)));
+    auto act_row = [&](int r) -> int {   // row in the resource, or -1
+      if (r >= w.rows) return -1;
+      if (!grouped) return r;
+      if (p.gather == nullptr) return w.p_begin + r;
+      const int slot = decltype(first)::value ? p.gather[w.p_begin + r] : next_slots[r];
+      return static_cast<unsigned>(slot) < static_cast<unsigned>(p.rows) ? slot / p.k_top : -1;
+    };
 #pragma unroll
-  for (int t = 0; t < S::copies_w; ++t) {
-    const int r = 8 * (wave + S::NW * t) + c_row;   // LDS row: fragment r / 16 % NF of wn = r / NR
-    const int m = r & 15, f = (r >> 4) % NF, w = r / NR;
-    int n;
-    if (kSwiglu) {
-      const int i = n0 + w * (NR / 2) + (m >> 2) * (2 * NF) + (f % (NF / 2)) * 4 + (m & 3);
-      n = f < NF / 2 ? i : half + i;
-    } else {
-      n = w * NR + (m >> 2) * (4 * NF) + f * 4 + (m & 3);
+    for (int t = 0; t < S::copies_a; ++t) {
+      const int row = act_row(8 * (wave + S::NW * t) + c_row);
+      aoff[t] = row < 0 ? kRsrcOutOfRange : static_cast<uint32_t>(row) * static_cast<uint32_t>(K) + c_piece;
     }
-    woff[t] = n < w_rows ? static_cast<uint32_t>(n) * static_cast<uint32_t>(K) + c_piece : kRsrcOutOfRange;
+    const int srow = act_row(64 * wave + lane);
+    soff = srow < 0 ? kRsrcOutOfRange : static_cast<uint32_t>(srow) * static_cast<uint32_t>(p.scale_row) * 4u;
+  };
+  // Scalar offsets stay within the resource (its range check subtracts them from its size).
+  auto run_of = [&](int kb, int first) {   // run of K that step kb takes
+    return kb >= nk ? 0 : S::Nt && kb + first >= nk ? kb + first - nk : kb + first;
+  };
+  // copy c of step kb's activations and scales
+  auto copy_a = [&](int c, int kb, int slot) {
+    const bool step = kb < nk;
+    const int run = run_of(kb, ak_first);
+    if (c == 0) {
+      const bool mine = wave < (S::TM + 63) / 64;
+      copy4(srs, step ? soff : kRsrcOutOfRange, static_cast<uint32_t>(run) * static_cast<uint32_t>(p.scale_k) * 4u,
+            lds0 + (mine ? S::s_at + slot * S::s_bytes + 256 * wave : S::dump_at));
+    } else {
+      const int j = wave + S::NW * (c - 1);
+      const uint32_t k0 = static_cast<uint32_t>(run) * 128u;
+      // past K (a short last run, or no step): zeros
+      copy16(ars, step && static_cast<int>(k0 + c_piece) < K ? aoff[c - 1] : kRsrcOutOfRange, k0,
+             lds0 + (j < S::TM / 8 ? S::a_at + slot * S::a_bytes + 1024 * j : S::dump_at));
+    }
+  };
+  // copy c of step kb's weights
+  auto copy_w = [&](int c, int kb, int slot) {
+    const bool step = kb < nk;
+    const uint32_t k0 = static_cast<uint32_t>(run_of(kb, wk_first)) * 128u;
+    const int d = weight_row(8 * S::NW * c) - weight_row(0);
+    const bool rows = d < w_rows;
+    copy16<S::Nt>(wrs, step && rows && static_cast<int>(k0 + c_piece) < K ? woff : kRsrcOutOfRange,
+                  rows ? static_cast<uint32_t>(d) * static_cast<uint32_t>(K) + k0 : 0u,
+                  lds0 + slot * S::w_bytes + 1024u * (wave + S::NW * c));
+  };
+  aim_w(cur);
+  aim_a(cur, std::true_type{});
+#pragma unroll
+  for (int s = -kW; s < 0; ++s) {
+    if (s + kA >= 0)
+#pragma unroll
+      for (int c = 0; c <= S::copies_a; ++c) copy_a(c, s + kA, s + kA);
+#pragma unroll
+    for (int c = 0; c < S::copies_w; ++c) copy_w(c, s + kW, s + kW);
   }
-  // activations and their scales: dense, a resource on the tile's rows; grouped, on all
-  const bool grouped = p.tiles != nullptr;
-  const int64_t a_first = grouped ? 0 : p_begin, a_count = grouped ? p.act_rows : rows;
-  const i32x4 ars = lds_rsrc(p.act + a_first * K, static_cast<uint32_t>(a_count * K));
-  const i32x4 srs = lds_rsrc(p.act_scale + a_first * p.scale_row,
-                             static_cast<uint32_t>(4 * (p.scale_k == 1 ? a_count * p.scale_row
-                                                                       : nk * p.scale_k)));
-  auto act_row = [&](int r) -> int64_t {   // row in the resource, or -1
-    if (r >= rows) return -1;
-    if (!grouped) return r;
-    if (p.gather == nullptr) return p_begin + r;
-    const int slot = p.gather[p_begin + r];
-    return static_cast<unsigned>(slot) < static_cast<unsigned>(p.rows) ? slot / p.k_top : -1;
-  };
-  uint32_t aoff[S::copies_a];
-#pragma unroll
-  for (int t = 0; t < S::copies_a; ++t) {
-    const int64_t row = act_row(8 * ((wave + S::NW * t) % (S::TM / 8)) + c_row);
-    aoff[t] = row < 0 ? kRsrcOutOfRange : static_cast<uint32_t>(row) * static_cast<uint32_t>(K) + c_piece;
-  }
-  const int64_t srow = act_row(64 * wave + lane);
-  const uint32_t soff = srow < 0 ? kRsrcOutOfRange : static_cast<uint32_t>(srow * p.scale_row * 4);
-  auto copy_step = [&](int kb, int slot) {
-    const uint32_t at = lds0 + slot * S::stage;
-    const uint32_t k0 = static_cast<uint32_t>(kb) * 128u;
-    const bool in = static_cast<int>(k0 + c_piece) < K;   // past K (a short last run, or no step): zeros
-#pragma unroll
-    for (int t = 0; t < S::copies_w; ++t)
-      copy16(wrs, in ? woff[t] : kRsrcOutOfRange, k0, at + 1024u * (wave + S::NW * t));
-#pragma unroll
-    for (int t = 0; t < S::copies_a; ++t)
-      copy16(ars, in ? aoff[t] : kRsrcOutOfRange, k0,
-             at + S::w_bytes + 1024u * ((wave + S::NW * t) % (S::TM / 8)));
-    copy4(srs, kb < nk ? soff : kRsrcOutOfRange, static_cast<uint32_t>(kb) * static_cast<uint32_t>(p.scale_k) * 4u,
-          at + S::w_bytes + S::a_bytes + 256u * wave);
-  };
-
-  // ---- weight scales: uniform, read through the constant cache
-  const int n_blk = (p.n + kFp8Block - 1) / kFp8Block;
-  const int col = n0 + wn * (kSwiglu ? NR / 2 : NR);
-  auto scale_row = [&](int n) {
-    const int b = n / kFp8Block < n_blk ? n / kFp8Block : n_blk - 1;   // past n: any (results unused)
-    const int64_t at = (static_cast<int64_t>(expert) * n_blk + __builtin_amdgcn_readfirstlane(b)) * nk;
-    return (const_float*)(p.w_scale + at);
-  };
-  const_float* ws0 = scale_row(col);
-  const_float* ws1 = scale_row(kSwiglu ? half + col : col);
-
-  floatx4 acc[MT][NF];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int f = 0; f < NF; ++f) acc[m][f] = floatx4{0.f, 0.f, 0.f, 0.f};
 
   const int place = r16 * 128 + 16 * (g ^ ((r16 >> 1) & 7));   // piece g; piece g + 4 is at ^ 64
-  const int my_rows = rows - wm * (S::TM / S::WM);              // rows of this wavefront's part
   auto read_frag = [&](const unsigned char* base, int row0) {
     const i32x4 lo = *reinterpret_cast<const i32x4*>(base + row0 * 128 + place);
     const i32x4 hi = *reinterpret_cast<const i32x4*>(base + row0 * 128 + (place ^ 64));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  // one step over the part's first NS activation fragments
-  auto step = [&](int kb, int slot, auto frags) {
-    constexpr int NS = decltype(frags)::value;
-    if constexpr (NS == 0) return;
-    const unsigned char* st = tile_lds + slot * S::stage;
-    const unsigned char* sa = st + S::w_bytes;
-    const float* ss = reinterpret_cast<const float*>(sa + S::a_bytes) + wm * (S::TM / S::WM) + r16;
-    const float w0 = ws0[kb], w1 = kSwiglu ? ws1[kb] : w0;
-    i32x8 a[NF];
-#pragma unroll
-    for (int f = 0; f < NF; ++f) a[f] = read_frag(st, wn * NR + 16 * f);
-    const unsigned char* mine = sa + wm * (S::TM / S::WM) * 128;
-    i32x8 b = read_frag(mine, 0);
-    float x = ss[0];
-#pragma unroll
-    for (int m = 0; m < NS; ++m) {
-      // the next fragment is read while this one multiplies; the compiler, left alone, reads
-      // all of them at once and spills
-      i32x8 b_next = b;
-      float x_next = x;
-      if (m + 1 < NS) {
-        b_next = read_frag(mine, 16 * (m + 1));
-        x_next = ss[16 * (m + 1)];
-      }
-      const float s0 = x * w0, s1 = kSwiglu ? x * w1 : s0;
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const floatx4 d = mfma_e4m3<kFull>(a[f], b);
-        const float s = f < NF / 2 ? s0 : s1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][f][i] = fmaf(d[i], s, acc[m][f][i]);
-      }
-      b = b_next;
-      x = x_next;
-      if (NS * NF > 16) __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  auto loop = [&](auto frags) {
-#pragma unroll
-    for (int s = 0; s < S::ST - 1; ++s) copy_step(s, s);
-    int slot = 0, fill = S::ST - 1;
-    for (int kb = 0; kb < nk; ++kb) {
-      wait_copies<(S::ST - 2) * S::copies>();   // this wavefront's copies of step kb are in LDS
-      barrier();                                // everybody's are, and step kb - 1 has been read
-      copy_step(kb + S::ST - 1, fill);
-      step(kb, slot, frags);
-      wait_lds();
-      slot = slot + 1 == S::ST ? 0 : slot + 1;
-      fill = fill + 1 == S::ST ? 0 : fill + 1;
-    }
-  };
-  // only fragments that hold rows are multiplied: the loop for 0, 1, 2, 4 .. MT of them, chosen
-  // per wavefront (uniform; every loop meets the same barriers)
-  const int need = (my_rows + 15) / 16;
-  if (need <= 0)
-    loop(std::integral_constant<int, 0>{});
-  else if (need <= 1)
-    loop(std::integral_constant<int, 1>{});
-  else if (MT <= 2 || need <= 2)
-    loop(std::integral_constant<int, MT < 2 ? MT : 2>{});
-  else if (MT <= 4 || need <= 4)
-    loop(std::integral_constant<int, MT < 4 ? MT : 4>{});
-  else
-    loop(std::integral_constant<int, MT>{});
+  const unsigned char* part = tile_lds + S::a_at + wm * (S::TM / S::WM) * 128;
+  const unsigned char* xpart = tile_lds + S::s_at + (wm * (S::TM / S::WM) + r16) * 4;
+  int wslot = 0, aslot = 0, wfill = kW % S::SW, afill = kA % S::SA;
+  for (;;) {
+    local += stride;
+    const Pair nxt = pair_at(local);
+    const bool more = nxt.tile < n_tiles;
+    const int rows = cur.rows, n0 = cur.n0;
+    const int64_t p_begin = cur.p_begin;   // 64-bit: output offsets
+    const int my_rows = rows - wm * (S::TM / S::WM);   // rows of this wavefront's part
 
-  // ---- results: lane has rows wm part + 16 m + r16, 4 NF (SwiGLU 2 NF) consecutive columns
-  if constexpr (kSwiglu) {
-    // h, quantised by runs of 128 columns: this workgroup's whole column block
-    static_assert(S::TN == 256 && NF % 2 == 0, "one run of h per workgroup");
-    wait_copies<0>();
-    barrier();   // LDS is free (the copies past the last step write zeros)
-    uint32_t* red = reinterpret_cast<uint32_t*>(tile_lds);   // [WN][TM] magnitudes
-    constexpr int HF = NF / 2;
+    // weight scales: uniform, read through the constant cache
+    const int col = n0 + wn * (kSwiglu ? NR / 2 : NR);
+    auto scale_row = [&](int n) {
+      const int b = n / kFp8Block < n_blk ? n / kFp8Block : n_blk - 1;   // past n: any (results unused)
+      return (const_float*)(p.w_scale + (static_cast<int64_t>(cur.expert) * n_blk + b) * nk);
+    };
+    const_float* ws0 = scale_row(col);
+    const_float* ws1 = scale_row(kSwiglu ? half + col : col);
+
+    floatx4 acc[MT][NF];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      uint32_t top = 0;
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int f = 0; f < HF; ++f)
+      for (int f = 0; f < NF; ++f) acc[m][f] = floatx4{0.f, 0.f, 0.f, 0.f};
+
+    // The K loop over the part's first NS activation fragments.  Within a step, fragment m's
+    // MFMAs are issued before fragment m - 1's multiply-adds, which then do not wait for their
+    // MFMAs, and fragment m + 1 is read meanwhile.  The step's barrier stands before its last
+    // fragment, when its LDS has been read: behind it the next step's weight fragments replace
+    // this one's as the last MFMAs take them, and the slot is filled again during the next
+    // step, a few copies a fragment (all at once, the wavefronts would stand at the full copy
+    // queue instead of multiplying).
+    auto loop = [&](auto frags) {
+      constexpr int NS = decltype(frags)::value;
+      constexpr int kOver = NS >= 4 ? NS / 2 : 1, kEach = (S::copies + kOver - 1) / kOver;
+      wait_copies<S::on_way + (kLate ? 0 : S::copies)>();
+      barrier();
+      if (kSwiglu && more) {   // the next tile's gather entries; in LDS before they are needed, as
+                               // every later wait for copies of this pair covers them
+        const int r = 64 * wave + lane;
+        const i32x4 grs = lds_rsrc(p.gather, static_cast<uint32_t>(p.rows) * 4u);
+        copy4(grs, r < nxt.rows ? static_cast<uint32_t>(nxt.p_begin + r) * 4u : kRsrcOutOfRange, 0,
+              lds0 + (wave < (S::TM + 63) / 64 ? S::slots_at + 256 * wave : S::dump_at));
+      }
+      i32x8 a[NF], b{};
+      float x = 0.f, w0 = ws0[cur.first], w1 = ws1[cur.first];
+      if constexpr (NS > 0) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float h = swiglu_fp8(acc[m][f][i], acc[m][HF + f][i], p.limit, p.clamp != 0);
-          acc[m][f][i] = h;
-          const uint32_t a = __float_as_uint(h) & 0x7FFFFFFFu;
-          top = a > top ? a : top;
+        for (int f = 0; f < NF; ++f) a[f] = read_frag(tile_lds + wslot * S::w_bytes, wn * NR + 16 * f);
+        b = read_frag(part + aslot * S::a_bytes, 0);
+        x = *reinterpret_cast<const float*>(xpart + aslot * S::s_bytes);
+      }
+      // the copies of this pair's steps, then of the next pair's first ones: weights first
+      int kb = 0, w_ahead = kW, a_ahead = kA;
+      auto copy_part = [&](int c, int k) {
+        if (c <= S::copies_a)
+          copy_a(c, k + a_ahead, afill);
+        else
+          copy_w(c - 1 - S::copies_a, k + w_ahead, wfill);
+      };
+#pragma unroll 1
+      for (int lap = 0; lap < 3; ++lap) {
+        const int end = lap == 0 ? steps - kW : lap == 1 ? steps - kA : steps;
+        if (lap == 1) {
+          w_ahead = more ? kW - steps : 1 << 20;   // no step: zeros
+          if (more) aim_w(nxt);
+        } else if (lap == 2) {
+          a_ahead = more ? kA - steps : 1 << 20;
+          if (more) aim_a(nxt, std::false_type{});
         }
+#pragma unroll 1
+        for (; kb < end; ++kb) {
+          const int wnext = wslot + 1 == S::SW ? 0 : wslot + 1, anext = aslot + 1 == S::SA ? 0 : aslot + 1;
+          int kn = kb + 1 < nk ? kb + 1 + cur.first : 0;
+          if (S::Nt && kn >= nk) kn -= nk;
+          const float w0n = ws0[kn], w1n = kSwiglu ? ws1[kn] : w0n;
+          floatx4 d[NF];
+          float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-      for (int d = 16; d < 64; d <<= 1) {
-        const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d, 64));
-        top = o > top ? o : top;
-      }
-      if (g == 0) red[wn * S::TM + wm * (S::TM / S::WM) + 16 * m + r16] = top;
-    }
-    wait_lds();
-    barrier();
-    uint8_t* hq = static_cast<uint8_t*>(p.out);
+          for (int m = 0; m < (NS > 0 ? NS : 1); ++m) {
+            const bool last = m + 1 >= NS;
+            if (kLate) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int r = wm * (S::TM / S::WM) + 16 * m + r16;
-      uint32_t top = 0;
+              for (int c = 0; c < S::copies; ++c)
+                if (c / kEach == m) copy_part(c, kb);
+            }
+            i32x8 b_next = b;
+            float x_next = x;
+            if (!last) {
+              b_next = read_frag(part + aslot * S::a_bytes, 16 * (m + 1));
+              x_next = *reinterpret_cast<const float*>(xpart + aslot * S::s_bytes + 64 * (m + 1));
+            } else {
+              wait_lds();
+              wait_copies<S::on_way>();   // this wavefront's copies of the next step
+              barrier();                  // everybody's; and this step has been read
+              if (!kLate) {
 #pragma unroll
-      for (int w = 0; w < S::WN; ++w) {
-        const uint32_t o = red[w * S::TM + r];
-        top = o > top ? o : top;
-      }
-      const bool finite = top < 0x7F800000u;
-      const RunScale q = run_scale(finite ? __uint_as_float(top) : 1.0f);
-      uint32_t o[HF];
+                for (int c = 0; c < S::copies; ++c) copy_part(c, kb);
+              }
+            }
+            if constexpr (NS > 0) {
+              if (m > 0) {   // keeps the multiply-adds of fragment m - 1 in this part of the code
 #pragma unroll
-      for (int f = 0; f < HF; ++f) {
-        const floatx4 h = acc[m][f];
-        o[f] = finite ? pack_e4m3(run_quotient(h[0], q), run_quotient(h[1], q), run_quotient(h[2], q),
-                                  run_quotient(h[3], q))
-                      : kNanCodes;
-      }
-      if (r >= rows) continue;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(hq + (p_begin + r) * p.ld_out + n0 + wn * (NR / 2) + g * (2 * NF));
-      if constexpr (HF == 2) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
-      } else {
+                for (int f = 0; f < NF; ++f) asm volatile("" : "+v"(d[f]));
+              }
+              floatx4 dn[NF];
+              const float t0 = x * w0, t1 = kSwiglu ? x * w1 : t0;
 #pragma unroll
-        for (int f = 0; f < HF; ++f) dst[f] = o[f];
-      }
-      if (wn == 0 && g == 0)
-        p.out_scale[static_cast<int64_t>(n0 / kFp8Block) * p.rows + p_begin + r] =
-            finite ? q.scale : __uint_as_float(0x7FC00000u);
-    }
-  } else {
-    const int c0 = n0 + wn * NR + g * (4 * NF);
-    const bool wide = p.n % 8 == 0;   // rows start on 16 bytes; columns come in whole eights
+              for (int f = 0; f < NF; ++f) {
+                dn[f] = mfma_e4m3<kFull>(a[f], b);
+                if (last) a[f] = read_frag(tile_lds + wnext * S::w_bytes, wn * NR + 16 * f);
+                if (m > 0) {
+                  const float s = f < NF / 2 ? s0 : s1;
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      const int r = wm * (S::TM / S::WM) + 16 * m + r16;
-      if (r >= rows) continue;
-      const int64_t at = (p_begin + r) * p.ld_out + c0;
-      if constexpr (kOut == kFp8OutF32) {
-        float* dst = static_cast<float*>(p.out) + at;
+                  for (int i = 0; i < 4; ++i) acc[m - 1][f][i] = fmaf(d[f][i], s, acc[m - 1][f][i]);
+                }
+              }
+              if (last) {
+                b_next = read_frag(part + anext * S::a_bytes, 0);
+                x_next = *reinterpret_cast<const float*>(xpart + anext * S::s_bytes);
+              }
 #pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          if (wide && c0 + 4 * f + 4 <= p.n) {
-            *reinterpret_cast<floatx4*>(dst + 4 * f) = acc[m][f];
-          } else {
+              for (int f = 0; f < NF; ++f) d[f] = dn[f];
+              s0 = t0;
+              s1 = t1;
+              b = b_next;
+              x = x_next;
+              if (NS * NF > 16) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (c0 + 4 * f + i < p.n) dst[4 * f + i] = acc[m][f][i];
+                for (int f = 0; f < NF; ++f) {
+                  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // one MFMA,
+                  __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read,
+                  __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);   // multiply-adds
+                }
+                __builtin_amdgcn_sched_barrier(0);
+              }
+            }
           }
+          if constexpr (NS > 0) {
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[NS - 1][f][i] = fmaf(d[f][i], f < NF / 2 ? s0 : s1, acc[NS - 1][f][i]);
+          }
+          w0 = w0n;
+          w1 = w1n;
+          wslot = wnext;
+          aslot = anext;
+          wfill = wfill + 1 == S::SW ? 0 : wfill + 1;
+          afill = afill + 1 == S::SA ? 0 : afill + 1;
         }
-      } else {
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + at;
+      }
+    };
+    // only fragments that hold rows are multiplied: the loop for 0, 1, 2, 4 .. MT of them, chosen
+    // per wavefront (uniform; every loop meets the same barriers)
+    const int need = (my_rows + 15) / 16;
+    if (need <= 0)
+      loop(std::integral_constant<int, 0>{});
+    else if (need <= 1)
+      loop(std::integral_constant<int, 1>{});
+    else if (MT <= 2 || need <= 2)
+      loop(std::integral_constant<int, MT < 2 ? MT : 2>{});
+    else if (MT <= 4 || need <= 4)
+      loop(std::integral_constant<int, MT < 4 ? MT : 4>{});
+    else
+      loop(std::integral_constant<int, MT>{});
+
+    // ---- results: lane has rows wm part + 16 m + r16, 4 NF (SwiGLU 2 NF) consecutive columns
+    if constexpr (kSwiglu) {
+      // h, quantised by runs of 128 columns: this workgroup's whole column block
+      static_assert(S::TN == 256 && NF % 2 == 0, "one run of h per workgroup");
+      uint32_t* red = reinterpret_cast<uint32_t*>(tile_lds + S::red_at);   // [WN][TM] magnitudes
+      constexpr int HF = NF / 2;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int f = 0; f < HF; ++f)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float h = swiglu_fp8(acc[m][f][i], acc[m][HF + f][i], p.limit, p.clamp != 0);
+            acc[m][f][i] = h;
+            const uint32_t a = __float_as_uint(h) & 0x7FFFFFFFu;
+            top = a > top ? a : top;
+          }
+#pragma unroll
+        for (int d = 16; d < 64; d <<= 1) {
+          const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d, 64));
+          top = o > top ? o : top;
+        }
+        if (g == 0) red[wn * S::TM + wm * (S::TM / S::WM) + 16 * m + r16] = top;
+      }
+      wait_lds();
+      barrier();
+      uint8_t* hq = static_cast<uint8_t*>(p.out);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int r = wm * (S::TM / S::WM) + 16 * m + r16;
+        uint32_t top = 0;
+#pragma unroll
+        for (int w = 0; w < S::WN; ++w) {
+          const uint32_t o = red[w * S::TM + r];
+          top = o > top ? o : top;
+        }
+        const bool finite = top < 0x7F800000u;
+        const RunScale q = run_scale(finite ? __uint_as_float(top) : 1.0f);
+        uint32_t o[HF];
+#pragma unroll
+        for (int f = 0; f < HF; ++f) {
+          const floatx4 h = acc[m][f];
+          o[f] = finite ? pack_e4m3(run_quotient(h[0], q), run_quotient(h[1], q), run_quotient(h[2], q),
+                                    run_quotient(h[3], q))
+                        : kNanCodes;
+        }
+        if (r >= rows) continue;
+        // streaming shapes gather a row's 128 bytes in LDS and store whole lines; the others write
+        // their 4 HF bytes
+        const int c = wn * (NR / 2) + g * (2 * NF);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(
+            S::Nt ? tile_lds + S::h_at + r * 128 + c
+                  : static_cast<unsigned char*>(hq) + (p_begin + r) * p.ld_out + n0 + c);
+        if constexpr (HF == 2) {
+          *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
+        } else {
+#pragma unroll
+          for (int f = 0; f < HF; ++f) dst[f] = o[f];
+        }
+        if (wn == 0 && g == 0)
+          p.out_scale[static_cast<int64_t>(n0 / kFp8Block) * p.rows + p_begin + r] =
+              finite ? q.scale : __uint_as_float(0x7FC00000u);
+      }
+      if constexpr (S::Nt) {
+        wait_lds();
+        barrier();
+        for (int i = threadIdx.x; i < rows * 8; i += S::threads)
+          store16(hq + (p_begin + i / 8) * p.ld_out + n0 + 16 * (i % 8),
+                  *reinterpret_cast<const i32x4*>(tile_lds + S::h_at + 16 * i));
+      }
+    } else {
+      // eight columns from 8 g on of every 32
+      const int c0 = n0 + wn * NR + 8 * g;
+      const bool wide = p.n % 8 == 0;   // rows start on 16 bytes; columns come in whole eights
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int r = wm * (S::TM / S::WM) + 16 * m + r16;
+        if (r >= rows) continue;
+        const int64_t at = (p_begin + r) * p.ld_out;
 #pragma unroll
         for (int f = 0; f < NF; f += 2) {
-          if (wide && c0 + 4 * f + 8 <= p.n) {
-            *reinterpret_cast<uint4*>(dst + 4 * f) =
-                make_uint4(pack_bf16x2(acc[m][f][0], acc[m][f][1]), pack_bf16x2(acc[m][f][2], acc[m][f][3]),
-                           pack_bf16x2(acc[m][f + 1][0], acc[m][f + 1][1]),
-                           pack_bf16x2(acc[m][f + 1][2], acc[m][f + 1][3]));
+          const int c = c0 + 16 * f;
+          if (wide && c < p.n) {
+            if constexpr (kOut == kFp8OutF32) {
+              store16(static_cast<float*>(p.out) + at + c, __builtin_bit_cast(i32x4, acc[m][f]));
+              store16(static_cast<float*>(p.out) + at + c + 4, __builtin_bit_cast(i32x4, acc[m][f + 1]));
+            } else {
+              store16(static_cast<uint16_t*>(p.out) + at + c,
+                      i32x4{static_cast<int>(pack_bf16x2(acc[m][f][0], acc[m][f][1])),
+                            static_cast<int>(pack_bf16x2(acc[m][f][2], acc[m][f][3])),
+                            static_cast<int>(pack_bf16x2(acc[m][f + 1][0], acc[m][f + 1][1])),
+                            static_cast<int>(pack_bf16x2(acc[m][f + 1][2], acc[m][f + 1][3]))});
+            }
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (c0 + 4 * f + i < p.n) dst[4 * f + i] = f32_to_bf16_bits(acc[m][f + i / 4][i % 4]);
+            for (int i = 0; i < 8; ++i) {
+              if (c + i >= p.n) break;
+              const float v = acc[m][f + i / 4][i % 4];
+              if constexpr (kOut == kFp8OutF32)
+                static_cast<float*>(p.out)[at + c + i] = v;
+              else
+                static_cast<uint16_t*>(p.out)[at + c + i] = f32_to_bf16_bits(v);
+            }
           }
         }
       }
     }
-    wait_copies<0>();   // no copy outlives its workgroup's LDS
+    if (!more) break;
+    cur = nxt;
   }
+  wait_copies<0>();   // no copy outlives its workgroup's LDS
 }
 
 template <class S, int kOut>
@@ -368,29 +549,41 @@ hipError_t launch(const Fp8Product& p, hipStream_t stream) {
   const int per = kOut == kFp8OutSwiglu ? S::TN / 2 : S::TN;
   const int col_blocks = (cols + per - 1) / per;
   const int64_t tiles = p.tiles ? p.tile_bound : (p.rows + S::TM - 1) / S::TM;
-  const int64_t work = (tiles + kXcds - 1) / kXcds * kXcds * col_blocks;
+  const int64_t pairs = (tiles + kXcds - 1) / kXcds * kXcds * col_blocks;
+  const int64_t most = static_cast<int64_t>(kFp8Cus) * S::per_cu;
   static const hipError_t attr = hipFuncSetAttribute(
       reinterpret_cast<const void*>(tile_kernel<S, kOut>), hipFuncAttributeMaxDynamicSharedMemorySize, S::lds);
   if (attr != hipSuccess) return attr;
-  tile_kernel<S, kOut><<<dim3(static_cast<unsigned>(work)), dim3(S::threads), S::lds, stream>>>(p, col_blocks, work);
+  tile_kernel<S, kOut><<<dim3(static_cast<unsigned>(pairs < most ? pairs : most)), dim3(S::threads), S::lds,
+                         stream>>>(p, col_blocks);
   return hipGetLastError();
+}
+
+// The streaming shapes of the grouped FFN: 16 and 32 rows, two or more workgroups' worth of ...
+template <int kOut>
+hipError_t launch_grouped(int tile_rows, const Fp8Product& p, hipStream_t stream) {
+  if (tile_rows == 16) return launch<Shape<16, 256, 1, 8, 4, 4, true>, kOut>(p, stream);
+  if (tile_rows == 32) return launch<Shape<32, 256, 1, 4, 2, 2, true>, kOut>(p, stream);
+  if (tile_rows == 96) return launch<Shape<96, 256, 2, 4, 3, 3, true>, kOut>(p, stream);
+  return launch<Shape<256, 256, 2, 4, 2, 2, false>, kOut>(p, stream);
 }
 
 }  // namespace
 
-hipError_t launch_fp8_tile(int tile_rows, const Fp8Product& p, hipStream_t stream) {
-  switch (p.out_kind) {
-    case kFp8OutSwiglu:
-      if (tile_rows <= 32) return launch<Shape<32, 256, 1, 4, 2>, kFp8OutSwiglu>(p, stream);
-      if (tile_rows <= 64) return launch<Shape<64, 256, 1, 4, 2>, kFp8OutSwiglu>(p, stream);
-      return launch<Shape<256, 256, 2, 4, 2>, kFp8OutSwiglu>(p, stream);
-    case kFp8OutF32:
-      return launch<Shape<64, 128, 1, 4, 3>, kFp8OutF32>(p, stream);
-    default:
-      if (tile_rows <= 32) return launch<Shape<32, 256, 1, 4, 2>, kFp8OutBf16>(p, stream);
-      if (tile_rows <= 64) return launch<Shape<64, 256, 1, 4, 2>, kFp8OutBf16>(p, stream);
-      return launch<Shape<256, 256, 2, 4, 2>, kFp8OutBf16>(p, stream);
-  }
+hipError_t launch_fp8_grouped(int tile_rows, const Fp8Product& p, hipStream_t stream) {
+  return p.out_kind == kFp8OutSwiglu ? launch_grouped<kFp8OutSwiglu>(tile_rows, p, stream)
+                                     : launch_grouped<kFp8OutBf16>(tile_rows, p, stream);
+}
+
+hipError_t launch_fp8_dense(const Fp8Product& p, hipStream_t stream) {
+  if (p.out_kind == kFp8OutF32) return launch<Shape<64, 128, 1, 4, 3, 3, false>, kFp8OutF32>(p, stream);
+  auto fits = [&](int tm, int tn) {
+    return (p.rows + tm - 1) / tm * ((p.n + tn - 1) / tn) <= kFp8Cus;
+  };
+  if (fits(64, 128)) return launch<Shape<64, 128, 2, 2, 3, 3, false>, kFp8OutBf16>(p, stream);
+  if (fits(128, 128)) return launch<Shape<128, 128, 2, 4, 4, 4, false>, kFp8OutBf16>(p, stream);
+  if (fits(128, 256)) return launch<Shape<128, 256, 2, 4, 3, 3, false>, kFp8OutBf16>(p, stream);
+  return launch<Shape<256, 256, 2, 4, 2, 2, false>, kFp8OutBf16>(p, stream);
 }
 
 }  // namespace moe

@@ -1,10 +1,10 @@
 // Rows to E4M3 elements with one scale per run of 128 (the rule: fp8_common.h).
 //
-// Sixteen lanes take a run, eight elements each: one 16-byte load (bf16; two for fp32),
+// Sixteen lanes take a run, eight elements each: one 16-byte load,
 // the run's maximum by four rotations of the 16-lane row, one 8-byte store; a wavefront
 // does four runs at a time.  Bound by the traffic, 3 bytes an element.
+#include "fp8.h"
 #include "fp8_common.h"
-#include "launch.h"
 
 namespace moe {
 namespace {
@@ -18,14 +18,7 @@ __device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
     v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
 }
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-
-template <class In>
-__global__ __launch_bounds__(256) void quantize_kernel(const In* __restrict__ x, int64_t runs, int K,
+__global__ __launch_bounds__(256) void quantize_kernel(const uint16_t* __restrict__ x, int64_t runs, int K,
                                                        int nb, uint8_t* __restrict__ q,
                                                        float* __restrict__ scale, int64_t scale_row,
                                                        int64_t scale_k) {
@@ -56,25 +49,15 @@ __global__ __launch_bounds__(256) void quantize_kernel(const In* __restrict__ x,
   if ((threadIdx.x & 15) == 0) scale[row * scale_row + b * scale_k] = finite ? s.scale : __uint_as_float(0x7FC00000u);
 }
 
-template <class In>
-hipError_t launch(const In* x, int64_t rows, int K, uint8_t* q, float* scale, int64_t scale_row,
-                  int64_t scale_k, hipStream_t stream) {
+}  // namespace
+
+hipError_t launch_quantize_fp8(const uint16_t* x, int64_t rows, int K, uint8_t* q, float* scale,
+                               int64_t scale_row, int64_t scale_k, hipStream_t stream) {
   const int nb = (K + kFp8Block - 1) / kFp8Block;
   const int64_t runs = rows * nb;
   quantize_kernel<<<dim3(static_cast<unsigned>((runs + 15) / 16)), dim3(256), 0, stream>>>(
       x, runs, K, nb, q, scale, scale_row, scale_k);
   return hipGetLastError();
-}
-
-}  // namespace
-
-hipError_t launch_quantize_fp8(const uint16_t* x, int64_t rows, int K, uint8_t* q, float* scale,
-                               int64_t scale_row, int64_t scale_k, hipStream_t stream) {
-  return launch(x, rows, K, q, scale, scale_row, scale_k, stream);
-}
-hipError_t launch_quantize_fp8_f32(const float* x, int64_t rows, int K, uint8_t* q, float* scale,
-                                   int64_t scale_row, int64_t scale_k, hipStream_t stream) {
-  return launch(x, rows, K, q, scale, scale_row, scale_k, stream);
 }
 
 }  // namespace moe

@@ -57,7 +57,6 @@ moe_status fp8_workspace_layout(int64_t T, int32_t E, int32_t k, int32_t H, int3
   L.xs = take(t * (H / 128) * sizeof(float));
   L.hq = take(slots * I);
   L.hs = take(slots * (I / 128) * sizeof(float));
-  L.h = L.tile_rows == 16 ? take(slots * I * sizeof(float)) : 0;
   L.plan = take(256 + static_cast<size_t>(L.tile_bound) * sizeof(RowTile));
   L.total = end > routing.offsets_bytes ? end : routing.offsets_bytes;
   *out = L;

@@ -9,7 +9,6 @@ namespace moe {
 struct Fp8WsLayout {
   size_t xq, xs;     // [T][H] codes, [T][H/128] scales
   size_t hq, hs;     // [T*k][I] codes, [T*k][I/128] scales
-  size_t h;          // fp32 [T*k][I]
   size_t plan;       // row-tile count, then the RowTile list
   size_t total;
   int64_t tile_bound;
