@@ -278,64 +278,66 @@ LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 FP8_BLOCK = 128
 
 
-class _Args:
-    """Pointers of one call's tensors, checked: dtype, shape, contiguity, one GPU."""
-
-    def __init__(self):
-        self.device = None
-
-    def ptr(self, t, dtype, shape, name):
-        if t.get_device() != self.device:
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a GPU tensor")
-            if self.device is not None:
-                raise ValueError(f"{name} is on another GPU than the other tensors")
-            self.device = t.get_device()
-        if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
-            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return t.data_ptr()
-
-    def ws(self, t):
-        if t is None:
-            return None, 0
-        return self.ptr(t, torch.uint8, t.shape, "ws"), t.numel()
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _run(fn: str, a: _Args, stream, *args):
+def _arg(t, dtype, shape, dev, name):
+    """Pointer of a tensor on GPU `dev`, checked: dtype, shape, contiguity.  The checks cost
+    about as much as the call's own launch, so there is one pass over a tensor's properties."""
+    if t.dtype is not dtype and not (dtype.__class__ is tuple and t.dtype in dtype):
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev or dev < 0:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        raise ValueError(f"{name} is on another GPU than the other tensors")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _ws(t, dev):
+    return (None, 0) if t is None else (_arg(t, torch.uint8, t.shape, dev, "ws"), t.numel())
+
+
+def _run(fn: str, dev: int, stream, *args):
+    """Calls entry point `fn` on `dev`'s current stream, or the stream given."""
     if stream is None:
-        handle = torch.cuda.current_stream(a.device).cuda_stream
+        handle = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
     else:
         handle = _stream(stream)
-    if a.device == torch.cuda.current_device():
-        code = getattr(load(), fn)(*args, handle)
+    call = getattr(_lib or load(), fn)
+    if dev == (_current_device() if _current_device else torch.cuda.current_device()):
+        code = call(*args, handle)
     else:
-        with torch.cuda.device(a.device):
-            code = getattr(load(), fn)(*args, handle)
-    _check(fn, code)
+        with torch.cuda.device(dev):
+            code = call(*args, handle)
+    if code:
+        raise MoeError(fn, code)
 
 
 def _runs(n: int) -> int:
     return -(-n // FP8_BLOCK)
 
 
-def _scored(a, logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups, group_top,
+def _scored(logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups, group_top,
             renormalize, scale):
     if logits.dim() != 2:
         raise ValueError("logits must be [T, E]")
     T, E = logits.shape
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
-    if logits.dtype not in LOGIT_TYPES:
+    kind = LOGIT_TYPES.get(logits.dtype)
+    if kind is None:
         raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
-    return (a.ptr(logits, logits.dtype, (T, E), "logits"), LOGIT_TYPES[logits.dtype], T, E, k,
-            SCORES[score], None if bias is None else a.ptr(bias, torch.float32, (E,), "bias"),
+    dev = logits.get_device()
+    return (_arg(logits, logits.dtype, (T, E), dev, "logits"), kind, T, E, k, SCORES[score],
+            None if bias is None else _arg(bias, torch.float32, (E,), dev, "bias"),
             groups, topk_groups, group_top, 1 if renormalize else 0, scale,
-            a.ptr(topk_ids, torch.int32, (T, k), "topk_ids"),
-            a.ptr(topk_weights, torch.float32, (T, k), "topk_weights"))
+            _arg(topk_ids, torch.int32, (T, k), dev, "topk_ids"),
+            _arg(topk_weights, torch.float32, (T, k), dev, "topk_weights"))
 
 
 def moe_route_scored(logits, k: int, topk_ids, topk_weights, *, score: str = "softmax", bias=None,
@@ -343,10 +345,9 @@ def moe_route_scored(logits, k: int, topk_ids, topk_weights, *, score: str = "so
                      renormalize: bool = True, scale: float = 1.0, stream=None):
     """Top-k over softmax or sigmoid scores plus a balance bias, within the best expert groups;
     weights are the chosen scores, renormalised or not, times `scale`."""
-    a = _Args()
-    _run("moe_route_scored", a, stream,
-         *_scored(a, logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups,
-                  group_top, renormalize, scale))
+    how = _scored(logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups, group_top,
+                  renormalize, scale)
+    _run("moe_route_scored", logits.get_device(), stream, *how)
 
 
 def moe_route_scored_and_group(logits, k: int, topk_ids, topk_weights, bitmatrix, counts, offsets,
@@ -354,25 +355,26 @@ def moe_route_scored_and_group(logits, k: int, topk_ids, topk_weights, bitmatrix
                                groups: int = 1, topk_groups: int = 1, group_top: int = 2,
                                renormalize: bool = True, scale: float = 1.0, stream=None):
     """moe_route_scored, moe_build_bitmatrix and moe_expert_offsets in one call."""
-    a = _Args()
-    how = _scored(a, logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups,
-                  group_top, renormalize, scale)
+    how = _scored(logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups, group_top,
+                  renormalize, scale)
     T, E = logits.shape
-    i32 = torch.int32
-    _run("moe_route_scored_and_group", a, stream, *how,
-         a.ptr(bitmatrix, i32, (T, (E + 31) // 32), "bitmatrix"), a.ptr(counts, i32, (E,), "counts"),
-         a.ptr(offsets, i32, (E + 1,), "offsets"), a.ptr(gather, i32, (T * k,), "gather"),
-         a.ptr(scatter, i32, (T * k,), "scatter"), *a.ws(ws))
+    dev, i32 = logits.get_device(), torch.int32
+    _run("moe_route_scored_and_group", dev, stream, *how,
+         _arg(bitmatrix, i32, (T, (E + 31) // 32), dev, "bitmatrix"),
+         _arg(counts, i32, (E,), dev, "counts"), _arg(offsets, i32, (E + 1,), dev, "offsets"),
+         _arg(gather, i32, (T * k,), dev, "gather"), _arg(scatter, i32, (T * k,), dev, "scatter"),
+         *_ws(ws, dev))
 
 
 def moe_quantize_fp8(x, q, scale, stream=None):
     """bf16 rows [rows, K] to E4M3 codes q [rows, K] with scale [rows, ceil(K / 128)]."""
-    a = _Args()
     if x.dim() != 2:
         raise ValueError("x must be [rows, K]")
     rows, K = x.shape
-    _run("moe_quantize_fp8", a, stream, a.ptr(x, BF16, (rows, K), "x"), rows, K,
-         a.ptr(q, E4M3, (rows, K), "q"), a.ptr(scale, torch.float32, (rows, _runs(K)), "scale"))
+    dev = x.get_device()
+    _run("moe_quantize_fp8", dev, stream, _arg(x, BF16, (rows, K), dev, "x"), rows, K,
+         _arg(q, E4M3, (rows, K), dev, "q"),
+         _arg(scale, torch.float32, (rows, _runs(K)), dev, "scale"))
 
 
 def moe_gemm_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -382,17 +384,16 @@ def moe_gemm_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
 def moe_gemm_fp8(xq, x_scale, w, w_scale, y, ws=None, stream=None):
     """y [M, N] (bf16 or fp32) = X W^T of block-scaled E4M3 xq [M, K] and w [N, K]; ws holds
     moe_gemm_fp8_workspace_bytes(M, N, K) bytes (None where that is 0)."""
-    a = _Args()
     if xq.dim() != 2 or w.dim() != 2:
         raise ValueError("xq must be [M, K] and w [N, K]")
     M, K = xq.shape
     N = w.shape[0]
-    kind = 0 if y.dtype == torch.float32 else 1
-    _run("moe_gemm_fp8", a, stream, a.ptr(xq, E4M3, (M, K), "xq"),
-         a.ptr(x_scale, torch.float32, (M, _runs(K)), "x_scale"), M, N, K,
-         a.ptr(w, E4M3, (N, K), "w"),
-         a.ptr(w_scale, torch.float32, (_runs(N), _runs(K)), "w_scale"), kind,
-         a.ptr(y, torch.float32 if kind == 0 else BF16, (M, N), "y"), *a.ws(ws))
+    dev, f32 = xq.get_device(), torch.float32
+    kind = 0 if y.dtype is f32 else 1
+    _run("moe_gemm_fp8", dev, stream, _arg(xq, E4M3, (M, K), dev, "xq"),
+         _arg(x_scale, f32, (M, _runs(K)), dev, "x_scale"), M, N, K,
+         _arg(w, E4M3, (N, K), dev, "w"), _arg(w_scale, f32, (_runs(N), _runs(K)), dev, "w_scale"),
+         kind, _arg(y, BF16 if kind else f32, (M, N), dev, "y"), *_ws(ws, dev))
 
 
 def moe_fp8_workspace_bytes(T: int, E: int, k: int, H: int, I: int) -> int:
@@ -403,17 +404,16 @@ def moe_grouped_ffn_fp8(x, k: int, w1, w1_scale, w2, w2_scale, counts, offsets, 
                         swiglu_limit: float, y_sorted, ws, stream=None):
     """The grouped expert FFN over block-scaled E4M3 weights w1 [E, 2I, H] (gate rows, then up
     rows) and w2 [E, H, I]; ws holds moe_fp8_workspace_bytes(T, E, k, H, I) bytes."""
-    a = _Args()
     if x.dim() != 2 or w1.dim() != 3 or w1.shape[1] % 2:
         raise ValueError("x must be [T, H] and w1 [E, 2I, H]")
     T, H = x.shape
     E, I = w1.shape[0], w1.shape[1] // 2
-    f32, i32 = torch.float32, torch.int32
-    _run("moe_grouped_ffn_fp8", a, stream, a.ptr(x, BF16, (T, H), "x"), T, H, I, E, k,
-         a.ptr(w1, E4M3, (E, 2 * I, H), "w1"),
-         a.ptr(w1_scale, f32, (E, _runs(2 * I), _runs(H)), "w1_scale"),
-         a.ptr(w2, E4M3, (E, H, I), "w2"),
-         a.ptr(w2_scale, f32, (E, _runs(H), _runs(I)), "w2_scale"),
-         a.ptr(counts, i32, (E,), "counts"), a.ptr(offsets, i32, (E + 1,), "offsets"),
-         a.ptr(gather, i32, (T * k,), "gather"), float(swiglu_limit),
-         a.ptr(y_sorted, BF16, (T * k, H), "y_sorted"), *a.ws(ws))
+    dev, f32, i32 = x.get_device(), torch.float32, torch.int32
+    _run("moe_grouped_ffn_fp8", dev, stream, _arg(x, BF16, (T, H), dev, "x"), T, H, I, E, k,
+         _arg(w1, E4M3, (E, 2 * I, H), dev, "w1"),
+         _arg(w1_scale, f32, (E, _runs(2 * I), _runs(H)), dev, "w1_scale"),
+         _arg(w2, E4M3, (E, H, I), dev, "w2"),
+         _arg(w2_scale, f32, (E, _runs(H), _runs(I)), dev, "w2_scale"),
+         _arg(counts, i32, (E,), dev, "counts"), _arg(offsets, i32, (E + 1,), dev, "offsets"),
+         _arg(gather, i32, (T * k,), dev, "gather"), swiglu_limit,
+         _arg(y_sorted, BF16, (T * k, H), dev, "y_sorted"), *_ws(ws, dev))

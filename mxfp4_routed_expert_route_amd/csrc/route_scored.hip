@@ -59,14 +59,14 @@ __global__ __launch_bounds__(1024) void scored_front_kernel(
 }
 
 ScoreArgs score_args(const ScoredRouting& r, int E) {
-  int g2 = 1;
-  while (g2 < r.groups) g2 *= 2;
-  return ScoreArgs{r.score,       r.bias,      r.groups,      E / r.groups, r.topk_groups,
-                   r.group_top,   r.renormalize, r.scale,     64 / g2};
+  int bits = 6;   // log2 of 64 / (groups rounded up to a power of two)
+  for (int g2 = 1; g2 < r.groups; g2 *= 2) --bits;
+  return ScoreArgs{r.score,     r.bias,        r.groups, E / r.groups, r.topk_groups,
+                   r.group_top, r.renormalize, r.scale,  bits};
 }
 
 // At most 32: per / L < 2 E / 64.
-int experts_per_lane(const ScoreArgs& a) { return (a.per + a.lanes - 1) / a.lanes; }
+int experts_per_lane(const ScoreArgs& a) { return (a.per + (1 << a.lane_bits) - 1) >> a.lane_bits; }
 // One launch up to this many experts per lane: with 16 wavefronts a workgroup has 128
 // registers a lane, and 16 or 32 experts per lane would spill there.
 constexpr int kFrontMaxPerLane = 8;
