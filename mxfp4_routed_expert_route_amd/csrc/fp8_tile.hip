@@ -85,23 +85,28 @@ struct Shape {
   static constexpr bool Nt = Nt_;
   static constexpr int NW = WM * WN, threads = 64 * NW;
   static constexpr int MT = TM / WM / 16, NF = TN / WN / 16;
-  // copies a wavefront issues in a step: scales, activations, weights, in this order
-  static constexpr int copies_w = TN / 8 / NW;
-  static constexpr int copies_a = (TM / 8 + NW - 1) / NW;
-  static constexpr int copies = 1 + copies_a + copies_w;
-  // copies that may be on their way when a step begins: the weights are SW - 1 steps ahead, the
-  // activations SA - 1
-  static constexpr int on_way = (SA - 2) * copies + (SW > SA ? copies_w : 0);
-  static constexpr int w_bytes = TN * 128, a_bytes = TM * 128, s_bytes = (TM + 63) / 64 * 256;
+  // 16-byte copies a wavefront issues in a step: activations, then weights.  The rows of
+  // activations may not go round evenly: the first `uneven` wavefronts have one more (0: all
+  // have copies_a).
+  static constexpr int copies_w = TN / 8 / NW, copies_a = (TM / 8 + NW - 1) / NW, uneven = TM / 8 % NW;
+  // Copies that may be on their way when a step begins, for a wavefront with `a` of activations:
+  // the weights are SW - 1 steps ahead, the activations SA - 1.
+  static constexpr int on_way(int a) { return (SA - 2) * (a + copies_w) + (SW > SA ? copies_w : 0); }
+  // Scales: one 4-byte copy a step for each 64 rows, by the wavefronts in turn and ahead of the
+  // step's other copies.  They are not counted: a wait for the others then also covers them, and
+  // one on its way makes a wait end a little later than it has to.  (A 4-byte copy takes a CU's
+  // address unit as long as two of the others: one by every wavefront in every step cost the
+  // 256 x 256 tile's step 107 of 690 ns of copies.)
+  static constexpr int scale_copies = (TM + 63) / 64 == 3 ? 4 : (TM + 63) / 64, turns = NW / scale_copies;
+  static constexpr int w_bytes = TN * 128, a_bytes = TM * 128, s_bytes = scale_copies * 256;
   static constexpr int a_at = SW * w_bytes, s_at = a_at + SA * a_bytes;
   static constexpr int red_at = s_at + SA * s_bytes;     // [WN][TM] magnitudes of h's runs
   static constexpr int slots_at = red_at + WN * TM * 4;  // gather entries of the next tile
-  static constexpr int dump_at = slots_at + s_bytes;     // where copies without rows write zeros
-  static constexpr int h_at = dump_at + 1024;            // [TM][128] codes of h
+  static constexpr int h_at = slots_at + s_bytes;        // [TM][128] codes of h
   static constexpr int lds = h_at + (Nt ? TM * 128 : 0);
   static constexpr int per_cu = 160 * 1024 / lds;        // workgroups of a CU
   static_assert(TN % (8 * NW) == 0 && NW % 2 == 0 && TM <= 64 * NW && per_cu >= 1, "shape");
-  static_assert(SA >= 2 && (SW == SA || SW == SA + 1), "order of the copies");
+  static_assert(SA >= 2 && (SW == SA || SW == SA + 1) && NW % scale_copies == 0, "order of the copies");
 };
 
 // Workgroups go through (row tile, column block) pairs; the copies run some steps ahead of the
@@ -210,28 +215,27 @@ void tile_kernel(Fp8Product p, int col_blocks) {
       const int row = act_row(8 * (wave + S::NW * t) + c_row);
       aoff[t] = row < 0 ? kRsrcOutOfRange : static_cast<uint32_t>(row) * static_cast<uint32_t>(K) + c_piece;
     }
-    const int srow = act_row(64 * wave + lane);
+    const int srow = act_row(64 * (wave % S::scale_copies) + lane);
     soff = srow < 0 ? kRsrcOutOfRange : static_cast<uint32_t>(srow) * static_cast<uint32_t>(p.scale_row) * 4u;
   };
   // Scalar offsets stay within the resource (its range check subtracts them from its size).
   auto run_of = [&](int kb, int first) {   // run of K that step kb takes
     return kb >= nk ? 0 : S::Nt && kb + first >= nk ? kb + first - nk : kb + first;
   };
-  // copy c of step kb's activations and scales
+  // step kb's scales, if it is this wavefront's turn
+  auto copy_s = [&](int kb, int slot) {
+    if (kb % S::turns == wave / S::scale_copies)   // uniform
+      copy4(srs, kb < nk ? soff : kRsrcOutOfRange,
+            static_cast<uint32_t>(run_of(kb, ak_first)) * static_cast<uint32_t>(p.scale_k) * 4u,
+            lds0 + S::s_at + slot * S::s_bytes + 256 * (wave % S::scale_copies));
+  };
+  // copy c of step kb's activations
   auto copy_a = [&](int c, int kb, int slot) {
-    const bool step = kb < nk;
-    const int run = run_of(kb, ak_first);
-    if (c == 0) {
-      const bool mine = wave < (S::TM + 63) / 64;
-      copy4(srs, step ? soff : kRsrcOutOfRange, static_cast<uint32_t>(run) * static_cast<uint32_t>(p.scale_k) * 4u,
-            lds0 + (mine ? S::s_at + slot * S::s_bytes + 256 * wave : S::dump_at));
-    } else {
-      const int j = wave + S::NW * (c - 1);
-      const uint32_t k0 = static_cast<uint32_t>(run) * 128u;
-      // past K (a short last run, or no step): zeros
-      copy16(ars, step && static_cast<int>(k0 + c_piece) < K ? aoff[c - 1] : kRsrcOutOfRange, k0,
-             lds0 + (j < S::TM / 8 ? S::a_at + slot * S::a_bytes + 1024 * j : S::dump_at));
-    }
+    if (S::uneven && c + 1 == S::copies_a && wave >= S::uneven) return;   // uniform
+    const uint32_t k0 = static_cast<uint32_t>(run_of(kb, ak_first)) * 128u;
+    // past K (a short last run, or no step): zeros
+    copy16(ars, kb < nk && static_cast<int>(k0 + c_piece) < K ? aoff[c] : kRsrcOutOfRange, k0,
+           lds0 + S::a_at + slot * S::a_bytes + 1024 * (wave + S::NW * c));
   };
   // copy c of step kb's weights
   auto copy_w = [&](int c, int kb, int slot) {
@@ -243,13 +247,24 @@ void tile_kernel(Fp8Product p, int col_blocks) {
                   rows ? static_cast<uint32_t>(d) * static_cast<uint32_t>(K) + k0 : 0u,
                   lds0 + slot * S::w_bytes + 1024u * (wave + S::NW * c));
   };
+  // waits until only copies on their way for later steps are left, and `more` steps' besides
+  auto wait_step = [&](auto more) {
+    constexpr int n = decltype(more)::value;
+    if (S::uneven && wave >= S::uneven)   // uniform
+      wait_copies<S::on_way(S::copies_a - 1) + n * (S::copies_a - 1 + S::copies_w)>();
+    else
+      wait_copies<S::on_way(S::copies_a) + n * (S::copies_a + S::copies_w)>();
+  };
   aim_w(cur);
   aim_a(cur, std::true_type{});
 #pragma unroll
   for (int s = -kW; s < 0; ++s) {
     if (s + kA >= 0)
+    {
+      copy_s(s + kA, s + kA);
 #pragma unroll
-      for (int c = 0; c <= S::copies_a; ++c) copy_a(c, s + kA, s + kA);
+      for (int c = 0; c < S::copies_a; ++c) copy_a(c, s + kA, s + kA);
+    }
 #pragma unroll
     for (int c = 0; c < S::copies_w; ++c) copy_w(c, s + kW, s + kW);
   }
@@ -295,15 +310,16 @@ void tile_kernel(Fp8Product p, int col_blocks) {
     // queue instead of multiplying).
     auto loop = [&](auto frags) {
       constexpr int NS = decltype(frags)::value;
-      constexpr int kOver = NS >= 4 ? NS / 2 : 1, kEach = (S::copies + kOver - 1) / kOver;
-      wait_copies<S::on_way + (kLate ? 0 : S::copies)>();
+      constexpr int kCopies = 1 + S::copies_a + S::copies_w;
+      constexpr int kOver = NS >= 4 ? NS / 2 : 1, kEach = (kCopies + kOver - 1) / kOver;
+      wait_step(std::integral_constant<int, kLate ? 0 : 1>{});
       barrier();
-      if (kSwiglu && more) {   // the next tile's gather entries; in LDS before they are needed, as
+      if (kSwiglu && more && wave < S::scale_copies) {   // the next tile's gather entries; in LDS before they are needed, as
                                // every later wait for copies of this pair covers them
         const int r = 64 * wave + lane;
         const i32x4 grs = lds_rsrc(p.gather, static_cast<uint32_t>(p.rows) * 4u);
         copy4(grs, r < nxt.rows ? static_cast<uint32_t>(nxt.p_begin + r) * 4u : kRsrcOutOfRange, 0,
-              lds0 + (wave < (S::TM + 63) / 64 ? S::slots_at + 256 * wave : S::dump_at));
+              lds0 + S::slots_at + 256 * wave);
       }
       i32x8 a[NF], b{};
       float x = 0.f, w0 = ws0[cur.first], w1 = ws1[cur.first];
@@ -316,8 +332,10 @@ void tile_kernel(Fp8Product p, int col_blocks) {
       // the copies of this pair's steps, then of the next pair's first ones: weights first
       int kb = 0, w_ahead = kW, a_ahead = kA;
       auto copy_part = [&](int c, int k) {
-        if (c <= S::copies_a)
-          copy_a(c, k + a_ahead, afill);
+        if (c == 0)
+          copy_s(k + a_ahead, afill);
+        else if (c <= S::copies_a)
+          copy_a(c - 1, k + a_ahead, afill);
         else
           copy_w(c - 1 - S::copies_a, k + w_ahead, wfill);
       };
@@ -344,7 +362,7 @@ void tile_kernel(Fp8Product p, int col_blocks) {
             const bool last = m + 1 >= NS;
             if (kLate) {
 #pragma unroll
-              for (int c = 0; c < S::copies; ++c)
+              for (int c = 0; c < kCopies; ++c)
                 if (c / kEach == m) copy_part(c, kb);
             }
             i32x8 b_next = b;
@@ -354,11 +372,11 @@ void tile_kernel(Fp8Product p, int col_blocks) {
               x_next = *reinterpret_cast<const float*>(xpart + aslot * S::s_bytes + 64 * (m + 1));
             } else {
               wait_lds();
-              wait_copies<S::on_way>();   // this wavefront's copies of the next step
-              barrier();                  // everybody's; and this step has been read
+              wait_step(std::integral_constant<int, 0>{});   // this wavefront's copies of the next step
+              barrier();                                     // everybody's; and this step has been read
               if (!kLate) {
 #pragma unroll
-                for (int c = 0; c < S::copies; ++c) copy_part(c, kb);
+                for (int c = 0; c < kCopies; ++c) copy_part(c, kb);
               }
             }
             if constexpr (NS > 0) {
