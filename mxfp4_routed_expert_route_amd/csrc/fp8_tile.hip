@@ -34,11 +34,12 @@ __device__ __forceinline__ i32x4 lds_rsrc(const void* base, uint32_t bytes) {
                __builtin_amdgcn_readfirstlane(static_cast<int>(u >> 32)),
                __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00020000};
 }
-// 16 (4) bytes a lane from rsrc + voff + soff to LDS address lds + 16 (4) * lane; offsets
-// voff past the resource give zeros.  In assembly so that the compiler, which cannot tell
-// the stages apart, does not wait for all copies before every LDS read; wait_copies counts
-// them.  They write no register.
-template <bool kNt = false>   // kNt: non-temporal
+// 16 bytes a lane from rsrc + voff + soff to LDS address lds + 16 * lane: 8 rows.  The resource's
+// range check takes voff alone: rows that are not there have to show in voff, and lanes past the
+// resource get zeros.  In assembly so that the compiler, which cannot tell the steps' LDS apart,
+// does not wait for all copies before every LDS read; wait_copies counts them.  They write no
+// register.
+template <bool kNt>   // kNt: non-temporal
 __device__ __forceinline__ void copy16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
   if constexpr (kNt)
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
@@ -47,6 +48,7 @@ __device__ __forceinline__ void copy16(i32x4 rsrc, uint32_t voff, uint32_t soff,
     asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
                  :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
 }
+// 4 bytes a lane from rsrc + voff + soff to LDS address lds + 4 * lane.
 __device__ __forceinline__ void copy4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
                :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
@@ -77,11 +79,14 @@ typedef __attribute__((address_space(4))) const int const_int;
 
 constexpr int kXcds = 8;
 
-// kNt: weights are read non-temporally (shapes whose weights are read about once).
-template <int TM_, int TN_, int WM_, int WN_, int SW_, int SA_, bool Nt_>
+// Nt: streaming shapes, whose weights are read about once: non-temporal copies of them, the
+// column blocks of a tile starting at different runs of K (so that the workgroups of the GPU,
+// which step together, do not all read the same columns of the weights, a few kB apart, at a
+// time: the 512-token burst's first product 684 -> 660 us), and whole-line stores of h.
+template <int TM_, int TN_, int WM_, int WN_, int ST_, bool Nt_>
 struct Shape {
   static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
-  static constexpr int SW = SW_, SA = SA_;               // steps of weights / of activations in LDS
+  static constexpr int ST = ST_;   // steps in LDS
   static constexpr bool Nt = Nt_;
   static constexpr int NW = WM * WN, threads = 64 * NW;
   static constexpr int MT = TM / WM / 16, NF = TN / WN / 16;
@@ -89,9 +94,6 @@ struct Shape {
   // activations may not go round evenly: the first `uneven` wavefronts have one more (0: all
   // have copies_a).
   static constexpr int copies_w = TN / 8 / NW, copies_a = (TM / 8 + NW - 1) / NW, uneven = TM / 8 % NW;
-  // Copies that may be on their way when a step begins, for a wavefront with `a` of activations:
-  // the weights are SW - 1 steps ahead, the activations SA - 1.
-  static constexpr int on_way(int a) { return (SA - 2) * (a + copies_w) + (SW > SA ? copies_w : 0); }
   // Scales: one 4-byte copy a step for each 64 rows, by the wavefronts in turn and ahead of the
   // step's other copies.  They are not counted: a wait for the others then also covers them, and
   // one on its way makes a wait end a little later than it has to.  (A 4-byte copy takes a CU's
@@ -99,14 +101,14 @@ struct Shape {
   // 256 x 256 tile's step 107 of 690 ns of copies.)
   static constexpr int scale_copies = (TM + 63) / 64 == 3 ? 4 : (TM + 63) / 64, turns = NW / scale_copies;
   static constexpr int w_bytes = TN * 128, a_bytes = TM * 128, s_bytes = scale_copies * 256;
-  static constexpr int a_at = SW * w_bytes, s_at = a_at + SA * a_bytes;
-  static constexpr int red_at = s_at + SA * s_bytes;     // [WN][TM] magnitudes of h's runs
+  static constexpr int a_at = ST * w_bytes, s_at = a_at + ST * a_bytes;
+  static constexpr int red_at = s_at + ST * s_bytes;     // [WN][TM] magnitudes of h's runs
   static constexpr int slots_at = red_at + WN * TM * 4;  // gather entries of the next tile
   static constexpr int h_at = slots_at + s_bytes;        // [TM][128] codes of h
   static constexpr int lds = h_at + (Nt ? TM * 128 : 0);
   static constexpr int per_cu = 160 * 1024 / lds;        // workgroups of a CU
-  static_assert(TN % (8 * NW) == 0 && NW % 2 == 0 && TM <= 64 * NW && per_cu >= 1, "shape");
-  static_assert(SA >= 2 && (SW == SA || SW == SA + 1) && NW % scale_copies == 0, "order of the copies");
+  static_assert(TM % 16 == 0 && TN % (16 * NW) == 0 && NW % scale_copies == 0 && per_cu >= 1, "shape");
+  static_assert(ST >= 2 && NW % 2 == 0, "copies");
 };
 
 // Workgroups go through (row tile, column block) pairs; the copies run some steps ahead of the
@@ -119,14 +121,14 @@ void tile_kernel(Fp8Product p, int col_blocks) {
   constexpr int MT = S::MT, NF = S::NF, NR = 16 * NF;
   // Steps the copies are ahead.  Streaming shapes fill a step's LDS as soon as its barrier says it
   // has been read; the others a little later, spread over the next step's fragments.
-  constexpr int kLate = S::Nt ? 0 : 1, kW = S::SW - kLate, kA = S::SA - kLate;
+  constexpr int kLate = S::Nt ? 0 : 1, kAhead = S::ST - kLate;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
   const int wm = wave / S::WN, wn = wave % S::WN;
   const int K = p.K, nk = (K + kFp8Block - 1) / kFp8Block;
   // steps past nk copy zeros; SwiGLU's next gather entries need some steps to arrive
-  constexpr int kLeast = kSwiglu ? 2 * kW : kW;
+  constexpr int kLeast = kSwiglu ? 2 * kAhead : kAhead;
   const int steps = nk < kLeast ? kLeast : nk;
   const int half = p.n / 2;
   const int n_blk = (p.n + kFp8Block - 1) / kFp8Block;
@@ -166,9 +168,10 @@ void tile_kernel(Fp8Product p, int col_blocks) {
   Pair cur = pair_at(local);
   if (cur.tile >= n_tiles) return;   // uniform
 
-  // ---- copies: this lane's place in a copy's 8 rows x 128 bytes, and the piece it fetches
-  const int c_row = lane >> 3;                                    // copy j: LDS row 8 j + c_row
-  const uint32_t c_piece = 16u * ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));   // j % 2 = wave % 2
+  // ---- copies: this lane's place in a copy's 8 rows x 128 bytes, and the piece it fetches.
+  // A wavefront's copy c goes to LDS rows 8 (wave + NW c) + c_row: all its copies odd or even.
+  const int c_row = lane >> 3;
+  const uint32_t c_piece = 16u * ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) unsigned char*)tile_lds));
   // weight row, from the column block's first, of an LDS row: fragment r / 16 % NF of wn = r / NR
@@ -178,30 +181,28 @@ void tile_kernel(Fp8Product p, int col_blocks) {
     const int i = v * (NR / 2) + (m >> 2) * (2 * NF) + (f % (NF / 2)) * 4 + (m & 3);
     return f < NF / 2 ? i : half + i;
   };
-  // a wavefront's copies are 8 NW LDS rows apart, whose weight rows are the same number of rows
-  // apart for every lane: a scalar offset
-  static_assert((S::NW / 2) % NF == 0 || NF % (S::NW / 2) == 0, "uniform distance of copies");
-  const uint32_t woff = static_cast<uint32_t>(weight_row(8 * wave + c_row)) * static_cast<uint32_t>(K) + c_piece;
+  // it is a lane part, weight_row(c_row), plus one that the wavefront shares
+  const uint32_t woff = static_cast<uint32_t>(weight_row(c_row)) * static_cast<uint32_t>(K) + c_piece;   // below 2^20
+  uint32_t wcopy[S::copies_w];
+#pragma unroll
+  for (int c = 0; c < S::copies_w; ++c)
+    wcopy[c] = static_cast<uint32_t>(weight_row(8 * (wave + S::NW * c))) * static_cast<uint32_t>(K);
+  const bool a_short = S::uneven && wave >= S::uneven;   // one copy of activations less
   i32x4 wrs, ars, srs;
-  int w_rows, wk_first, ak_first;
+  int w_first, a_first;
   uint32_t aoff[S::copies_a], soff;
   const int* next_slots = reinterpret_cast<const int*>(tile_lds + S::slots_at);
-  auto aim_w = [&](const Pair& w) {
-    // weights: a resource from the column block's first row on, to the expert's last (SwiGLU) or
-    // the block's last
+  // aims the copies at a pair; its gather entries: read here (first pair) or from LDS
+  auto aim = [&](const Pair& w, auto first) {
+    // weights: from the column block's first row on, to the expert's last (SwiGLU) or the block's
     const uint8_t* wbase = p.w + (static_cast<int64_t>(w.expert) * p.n + w.n0) * K;
-    w_rows = kSwiglu ? p.n - w.n0 : (p.n - w.n0 < S::TN ? p.n - w.n0 : S::TN);
+    const int w_rows = kSwiglu ? p.n - w.n0 : (p.n - w.n0 < S::TN ? p.n - w.n0 : S::TN);
     wrs = lds_rsrc(wbase, static_cast<uint32_t>(static_cast<int64_t>(w_rows) * K));
-    wk_first = w.first;
-  };
-  // its gather entries: read here (first pair) or from LDS
-  auto aim_a = [&](const Pair& w, auto first) {
-    ak_first = w.first;
     // activations and their scales: dense, a resource on the tile's rows; grouped, on all
-    const int64_t a_first = grouped ? 0 : w.p_begin;
+    const int64_t a_row0 = grouped ? 0 : w.p_begin;
     const int64_t a_count = grouped ? p.act_rows : static_cast<int64_t>(w.rows);
-    ars = lds_rsrc(p.act + a_first * K, static_cast<uint32_t>(a_count * K));
-    srs = lds_rsrc(p.act_scale + a_first * p.scale_row,
+    ars = lds_rsrc(p.act + a_row0 * K, static_cast<uint32_t>(a_count * K));
+    srs = lds_rsrc(p.act_scale + a_row0 * p.scale_row,
                    static_cast<uint32_t>(4 * ((a_count - 1) * p.scale_row + (nk - 1) * p.scale_k + 1)));
     auto act_row = [&](int r) -> int {   // row in the resource, or -1
       if (r >= w.rows) return -1;
@@ -211,62 +212,64 @@ void tile_kernel(Fp8Product p, int col_blocks) {
       return static_cast<unsigned>(slot) < static_cast<unsigned>(p.rows) ? slot / p.k_top : -1;
     };
 #pragma unroll
-    for (int t = 0; t < S::copies_a; ++t) {
-      const int row = act_row(8 * (wave + S::NW * t) + c_row);
-      aoff[t] = row < 0 ? kRsrcOutOfRange : static_cast<uint32_t>(row) * static_cast<uint32_t>(K) + c_piece;
+    for (int c = 0; c < S::copies_a; ++c) {
+      const int row = act_row(8 * (wave + S::NW * c) + c_row);
+      aoff[c] = row < 0 ? kRsrcOutOfRange : static_cast<uint32_t>(row) * static_cast<uint32_t>(K) + c_piece;
     }
     const int srow = act_row(64 * (wave % S::scale_copies) + lane);
     soff = srow < 0 ? kRsrcOutOfRange : static_cast<uint32_t>(srow) * static_cast<uint32_t>(p.scale_row) * 4u;
+    w_first = a_first = w.first;
   };
-  // Scalar offsets stay within the resource (its range check subtracts them from its size).
-  auto run_of = [&](int kb, int first) {   // run of K that step kb takes
+  auto run_of = [&](int kb, int first) {   // run of K that step kb takes; past the last: any
     return kb >= nk ? 0 : S::Nt && kb + first >= nk ? kb + first - nk : kb + first;
   };
+  const int short_run = K % kFp8Block ? nk - 1 : -1;   // the run that ends early
   // step kb's scales, if it is this wavefront's turn
   auto copy_s = [&](int kb, int slot) {
-    if (kb % S::turns == wave / S::scale_copies)   // uniform
-      copy4(srs, kb < nk ? soff : kRsrcOutOfRange,
-            static_cast<uint32_t>(run_of(kb, ak_first)) * static_cast<uint32_t>(p.scale_k) * 4u,
+    if (static_cast<int>(static_cast<unsigned>(kb) % S::turns) == wave / S::scale_copies)   // uniform
+      copy4(srs, soff, static_cast<uint32_t>(run_of(kb, a_first)) * static_cast<uint32_t>(p.scale_k) * 4u,
             lds0 + S::s_at + slot * S::s_bytes + 256 * (wave % S::scale_copies));
   };
-  // copy c of step kb's activations
+  // copy c of step kb's activations.  Past the last run they are not zeros, but the weights are.
   auto copy_a = [&](int c, int kb, int slot) {
-    if (S::uneven && c + 1 == S::copies_a && wave >= S::uneven) return;   // uniform
-    const uint32_t k0 = static_cast<uint32_t>(run_of(kb, ak_first)) * 128u;
-    // past K (a short last run, or no step): zeros
-    copy16(ars, kb < nk && static_cast<int>(k0 + c_piece) < K ? aoff[c] : kRsrcOutOfRange, k0,
-           lds0 + S::a_at + slot * S::a_bytes + 1024 * (wave + S::NW * c));
+    if (c + 1 == S::copies_a && a_short) return;   // uniform
+    const int run = run_of(kb, a_first);
+    const uint32_t k0 = static_cast<uint32_t>(run) * 128u;
+    uint32_t v = aoff[c];
+    if (run == short_run) v = static_cast<int>(k0 + c_piece) < K ? v : kRsrcOutOfRange;   // zeros past K
+    copy16<false>(ars, v, k0, lds0 + S::a_at + slot * S::a_bytes + 1024 * (wave + S::NW * c));
   };
-  // copy c of step kb's weights
+  // copy c of step kb's weights; zeros past the last run
   auto copy_w = [&](int c, int kb, int slot) {
-    const bool step = kb < nk;
-    const uint32_t k0 = static_cast<uint32_t>(run_of(kb, wk_first)) * 128u;
-    const int d = weight_row(8 * S::NW * c) - weight_row(0);
-    const bool rows = d < w_rows;
-    copy16<S::Nt>(wrs, step && rows && static_cast<int>(k0 + c_piece) < K ? woff : kRsrcOutOfRange,
-                  rows ? static_cast<uint32_t>(d) * static_cast<uint32_t>(K) + k0 : 0u,
-                  lds0 + slot * S::w_bytes + 1024u * (wave + S::NW * c));
+    const int run = run_of(kb, w_first);
+    const uint32_t k0 = static_cast<uint32_t>(run) * 128u;
+    // no step: kRsrcOutOfRange and up, with less than 2^20 to add
+    uint32_t v = woff + (kb < nk ? wcopy[c] : kRsrcOutOfRange);
+    if (run == short_run) v = static_cast<int>(k0 + c_piece) < K ? v : kRsrcOutOfRange;
+    copy16<S::Nt>(wrs, v, k0, lds0 + slot * S::w_bytes + 1024 * (wave + S::NW * c));
+  };
+  constexpr int kCopies = 1 + S::copies_a + S::copies_w;
+  auto copy_part = [&](int c, int kb, int slot) {
+    if (c == 0)
+      copy_s(kb, slot);
+    else if (c <= S::copies_a)
+      copy_a(c - 1, kb, slot);
+    else
+      copy_w(c - 1 - S::copies_a, kb, slot);
   };
   // waits until only copies on their way for later steps are left, and `more` steps' besides
   auto wait_step = [&](auto more) {
-    constexpr int n = decltype(more)::value;
-    if (S::uneven && wave >= S::uneven)   // uniform
-      wait_copies<S::on_way(S::copies_a - 1) + n * (S::copies_a - 1 + S::copies_w)>();
+    constexpr int n = S::ST - 2 + decltype(more)::value;
+    if (a_short)   // uniform
+      wait_copies<n * (S::copies_a - 1 + S::copies_w)>();
     else
-      wait_copies<S::on_way(S::copies_a) + n * (S::copies_a + S::copies_w)>();
+      wait_copies<n * (S::copies_a + S::copies_w)>();
   };
-  aim_w(cur);
-  aim_a(cur, std::true_type{});
+  aim(cur, std::true_type{});
 #pragma unroll
-  for (int s = -kW; s < 0; ++s) {
-    if (s + kA >= 0)
-    {
-      copy_s(s + kA, s + kA);
+  for (int s = 0; s < kAhead; ++s) {
 #pragma unroll
-      for (int c = 0; c < S::copies_a; ++c) copy_a(c, s + kA, s + kA);
-    }
-#pragma unroll
-    for (int c = 0; c < S::copies_w; ++c) copy_w(c, s + kW, s + kW);
+    for (int c = 0; c < kCopies; ++c) copy_part(c, s, s);
   }
 
   const int place = r16 * 128 + 16 * (g ^ ((r16 >> 1) & 7));   // piece g; piece g + 4 is at ^ 64
@@ -277,7 +280,7 @@ void tile_kernel(Fp8Product p, int col_blocks) {
   };
   const unsigned char* part = tile_lds + S::a_at + wm * (S::TM / S::WM) * 128;
   const unsigned char* xpart = tile_lds + S::s_at + (wm * (S::TM / S::WM) + r16) * 4;
-  int wslot = 0, aslot = 0, wfill = kW % S::SW, afill = kA % S::SA;
+  int slot = 0, fill = kAhead % S::ST;
   for (;;) {
     local += stride;
     const Pair nxt = pair_at(local);
@@ -310,12 +313,11 @@ void tile_kernel(Fp8Product p, int col_blocks) {
     // queue instead of multiplying).
     auto loop = [&](auto frags) {
       constexpr int NS = decltype(frags)::value;
-      constexpr int kCopies = 1 + S::copies_a + S::copies_w;
-      constexpr int kOver = NS >= 4 ? NS / 2 : 1, kEach = (kCopies + kOver - 1) / kOver;
       wait_step(std::integral_constant<int, kLate ? 0 : 1>{});
       barrier();
-      if (kSwiglu && more && wave < S::scale_copies) {   // the next tile's gather entries; in LDS before they are needed, as
-                               // every later wait for copies of this pair covers them
+      if (kSwiglu && more && wave < S::scale_copies) {
+        // the next tile's gather entries: in LDS before they are needed, as the waits of this pair's
+        // later steps cover them
         const int r = 64 * wave + lane;
         const i32x4 grs = lds_rsrc(p.gather, static_cast<uint32_t>(p.rows) * 4u);
         copy4(grs, r < nxt.rows ? static_cast<uint32_t>(nxt.p_begin + r) * 4u : kRsrcOutOfRange, 0,
@@ -325,33 +327,22 @@ void tile_kernel(Fp8Product p, int col_blocks) {
       float x = 0.f, w0 = ws0[cur.first], w1 = ws1[cur.first];
       if constexpr (NS > 0) {
 #pragma unroll
-        for (int f = 0; f < NF; ++f) a[f] = read_frag(tile_lds + wslot * S::w_bytes, wn * NR + 16 * f);
-        b = read_frag(part + aslot * S::a_bytes, 0);
-        x = *reinterpret_cast<const float*>(xpart + aslot * S::s_bytes);
+        for (int f = 0; f < NF; ++f) a[f] = read_frag(tile_lds + slot * S::w_bytes, wn * NR + 16 * f);
+        b = read_frag(part + slot * S::a_bytes, 0);
+        x = *reinterpret_cast<const float*>(xpart + slot * S::s_bytes);
       }
-      // the copies of this pair's steps, then of the next pair's first ones: weights first
-      int kb = 0, w_ahead = kW, a_ahead = kA;
-      auto copy_part = [&](int c, int k) {
-        if (c == 0)
-          copy_s(k + a_ahead, afill);
-        else if (c <= S::copies_a)
-          copy_a(c - 1, k + a_ahead, afill);
-        else
-          copy_w(c - 1 - S::copies_a, k + w_ahead, wfill);
-      };
+      // the copies of this pair's steps, then of the next pair's first ones
+      int kb = 0, ahead = kAhead;
 #pragma unroll 1
-      for (int lap = 0; lap < 3; ++lap) {
-        const int end = lap == 0 ? steps - kW : lap == 1 ? steps - kA : steps;
+      for (int lap = 0; lap < 2; ++lap) {
+        const int end = lap == 0 ? steps - kAhead : steps;
         if (lap == 1) {
-          w_ahead = more ? kW - steps : 1 << 20;   // no step: zeros
-          if (more) aim_w(nxt);
-        } else if (lap == 2) {
-          a_ahead = more ? kA - steps : 1 << 20;
-          if (more) aim_a(nxt, std::false_type{});
+          ahead = more ? kAhead - steps : 1 << 20;   // no step: zeros
+          if (more) aim(nxt, std::false_type{});
         }
 #pragma unroll 1
         for (; kb < end; ++kb) {
-          const int wnext = wslot + 1 == S::SW ? 0 : wslot + 1, anext = aslot + 1 == S::SA ? 0 : aslot + 1;
+          const int next = slot + 1 == S::ST ? 0 : slot + 1;
           int kn = kb + 1 < nk ? kb + 1 + cur.first : 0;
           if (S::Nt && kn >= nk) kn -= nk;
           const float w0n = ws0[kn], w1n = kSwiglu ? ws1[kn] : w0n;
@@ -360,23 +351,29 @@ void tile_kernel(Fp8Product p, int col_blocks) {
 #pragma unroll
           for (int m = 0; m < (NS > 0 ? NS : 1); ++m) {
             const bool last = m + 1 >= NS;
-            if (kLate) {
+            // Where the copies go: streaming shapes, at once behind the barrier; the 256 x 256 tile,
+            // some ahead of each of the first half's fragments; the others, behind the first
+            // fragment's MFMAs (a CU takes in one such copy every 16 cycles, and the wavefronts
+            // stand meanwhile), unless the step has no other fragment before its wait.
+            constexpr bool kAfter = kLate && NS >= 2 && MT * NF <= 16;
+            constexpr int kOver = NS >= 4 ? NS / 2 : 1, kEach = (kCopies + kOver - 1) / kOver;
+            if (kLate && !kAfter) {
 #pragma unroll
               for (int c = 0; c < kCopies; ++c)
-                if (c / kEach == m) copy_part(c, kb);
+                if (c / kEach == m) copy_part(c, kb + ahead, fill);
             }
             i32x8 b_next = b;
             float x_next = x;
             if (!last) {
-              b_next = read_frag(part + aslot * S::a_bytes, 16 * (m + 1));
-              x_next = *reinterpret_cast<const float*>(xpart + aslot * S::s_bytes + 64 * (m + 1));
+              b_next = read_frag(part + slot * S::a_bytes, 16 * (m + 1));
+              x_next = *reinterpret_cast<const float*>(xpart + slot * S::s_bytes + 64 * (m + 1));
             } else {
               wait_lds();
               wait_step(std::integral_constant<int, 0>{});   // this wavefront's copies of the next step
               barrier();                                     // everybody's; and this step has been read
               if (!kLate) {
 #pragma unroll
-                for (int c = 0; c < kCopies; ++c) copy_part(c, kb);
+                for (int c = 0; c < kCopies; ++c) copy_part(c, kb + ahead, fill);
               }
             }
             if constexpr (NS > 0) {
@@ -389,7 +386,7 @@ void tile_kernel(Fp8Product p, int col_blocks) {
 #pragma unroll
               for (int f = 0; f < NF; ++f) {
                 dn[f] = mfma_e4m3<kFull>(a[f], b);
-                if (last) a[f] = read_frag(tile_lds + wnext * S::w_bytes, wn * NR + 16 * f);
+                if (last) a[f] = read_frag(tile_lds + next * S::w_bytes, wn * NR + 16 * f);
                 if (m > 0) {
                   const float s = f < NF / 2 ? s0 : s1;
 #pragma unroll
@@ -397,8 +394,13 @@ void tile_kernel(Fp8Product p, int col_blocks) {
                 }
               }
               if (last) {
-                b_next = read_frag(part + anext * S::a_bytes, 0);
-                x_next = *reinterpret_cast<const float*>(xpart + anext * S::s_bytes);
+                b_next = read_frag(part + next * S::a_bytes, 0);
+                x_next = *reinterpret_cast<const float*>(xpart + next * S::s_bytes);
+              }
+              if (kAfter && m == 0) {
+                __builtin_amdgcn_sched_barrier(0);   // the MFMAs first
+#pragma unroll
+                for (int c = 0; c < kCopies; ++c) copy_part(c, kb + ahead, fill);
               }
 #pragma unroll
               for (int f = 0; f < NF; ++f) d[f] = dn[f];
@@ -426,10 +428,8 @@ void tile_kernel(Fp8Product p, int col_blocks) {
           }
           w0 = w0n;
           w1 = w1n;
-          wslot = wnext;
-          aslot = anext;
-          wfill = wfill + 1 == S::SW ? 0 : wfill + 1;
-          afill = afill + 1 == S::SA ? 0 : afill + 1;
+          slot = next;
+          fill = fill + 1 == S::ST ? 0 : fill + 1;
         }
       }
     };
@@ -577,13 +577,14 @@ hipError_t launch(const Fp8Product& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The streaming shapes of the grouped FFN: 16 and 32 rows, two or more workgroups' worth of ...
+// fp8_tile_rows has the rule for the rows.  Up to 96 rows the weights are the traffic; at 32 rows
+// two workgroups fit a CU and cover each other's barriers and stores.
 template <int kOut>
 hipError_t launch_grouped(int tile_rows, const Fp8Product& p, hipStream_t stream) {
-  if (tile_rows == 16) return launch<Shape<16, 256, 1, 8, 4, 4, true>, kOut>(p, stream);
-  if (tile_rows == 32) return launch<Shape<32, 256, 1, 4, 2, 2, true>, kOut>(p, stream);
-  if (tile_rows == 96) return launch<Shape<96, 256, 2, 4, 3, 3, true>, kOut>(p, stream);
-  return launch<Shape<256, 256, 2, 4, 2, 2, false>, kOut>(p, stream);
+  if (tile_rows == 16) return launch<Shape<16, 256, 1, 8, 4, true>, kOut>(p, stream);
+  if (tile_rows == 32) return launch<Shape<32, 256, 1, 4, 2, true>, kOut>(p, stream);
+  if (tile_rows == 96) return launch<Shape<96, 256, 2, 4, 3, true>, kOut>(p, stream);
+  return launch<Shape<256, 256, 2, 4, 2, false>, kOut>(p, stream);
 }
 
 }  // namespace
@@ -594,14 +595,14 @@ hipError_t launch_fp8_grouped(int tile_rows, const Fp8Product& p, hipStream_t st
 }
 
 hipError_t launch_fp8_dense(const Fp8Product& p, hipStream_t stream) {
-  if (p.out_kind == kFp8OutF32) return launch<Shape<64, 128, 1, 4, 3, 3, false>, kFp8OutF32>(p, stream);
+  if (p.out_kind == kFp8OutF32) return launch<Shape<64, 128, 1, 4, 3, false>, kFp8OutF32>(p, stream);
   auto fits = [&](int tm, int tn) {
     return (p.rows + tm - 1) / tm * ((p.n + tn - 1) / tn) <= kFp8Cus;
   };
-  if (fits(64, 128)) return launch<Shape<64, 128, 2, 2, 3, 3, false>, kFp8OutBf16>(p, stream);
-  if (fits(128, 128)) return launch<Shape<128, 128, 2, 4, 4, 4, false>, kFp8OutBf16>(p, stream);
-  if (fits(128, 256)) return launch<Shape<128, 256, 2, 4, 3, 3, false>, kFp8OutBf16>(p, stream);
-  return launch<Shape<256, 256, 2, 4, 2, 2, false>, kFp8OutBf16>(p, stream);
+  if (fits(64, 128)) return launch<Shape<64, 128, 2, 2, 3, false>, kFp8OutBf16>(p, stream);
+  if (fits(128, 128)) return launch<Shape<128, 128, 2, 4, 4, false>, kFp8OutBf16>(p, stream);
+  if (fits(128, 256)) return launch<Shape<128, 256, 2, 4, 3, false>, kFp8OutBf16>(p, stream);
+  return launch<Shape<256, 256, 2, 4, 2, false>, kFp8OutBf16>(p, stream);
 }
 
 }  // namespace moe

@@ -411,3 +411,27 @@ def test_binding_refuses_wrong_shapes_on_the_gpu():
         binding.moe_gemm_fp8(q, s, q, s, x)
     with pytest.raises(binding.MoeError):
         binding.moe_quantize_fp8(x[:, :8].contiguous(), q[:, :8].contiguous(), s[:, :1].contiguous())
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 129, 272), (70, 261, 400), (300, 520, 656), (1100, 4104, 144)])
+@pytest.mark.parametrize("f32", [True, False])
+def test_gemm_beside_other_tensors(m, n, k, f32):
+    """Operands that end inside larger allocations: what stands behind their last rows (NaN codes,
+    NaN scales) reaches no result, and the output's neighbours stay as they were."""
+    from mxfp4_routed_expert_route_amd import binding
+    say("beside", m, n, k, f32)
+    rng = np.random.default_rng(m + n)
+    nk, nb = -(-k // 128), -(-n // 128)
+    xq, w, xs, ws = codes(rng, m, k), codes(rng, n, k), scales(rng, m, nk), scales(rng, nb, nk)
+
+    def inside(a, rows, fill):
+        return cuda(np.concatenate([a, np.full((rows,) + a.shape[1:], fill, a.dtype)]))[:a.shape[0]]
+
+    y = gpu_gemm(xq, xs, w, ws, f32)
+    out = torch.full((m + 64, n), 7.0, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    binding.moe_gemm_fp8(inside(xq, 300, 0x7F), inside(xs, 300, np.nan), inside(w, 300, 0x7F),
+                         inside(ws, 3, np.nan), out[:m])
+    torch.cuda.synchronize()
+    assert np.isfinite(y).all()
+    assert np.array_equal(out[:m].float().cpu().numpy(), y.astype(np.float32))
+    assert (out[m:] == 7.0).all()
