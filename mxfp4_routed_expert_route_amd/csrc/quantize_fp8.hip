@@ -54,10 +54,16 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t* __restric
 hipError_t launch_quantize_fp8(const uint16_t* x, int64_t rows, int K, uint8_t* q, float* scale,
                                int64_t scale_row, int64_t scale_k, hipStream_t stream) {
   const int nb = (K + kFp8Block - 1) / kFp8Block;
-  const int64_t runs = rows * nb;
-  quantize_kernel<<<dim3(static_cast<unsigned>((runs + 15) / 16)), dim3(256), 0, stream>>>(
-      x, runs, K, nb, q, scale, scale_row, scale_k);
-  return hipGetLastError();
+  // a launch has fewer than 2^32 threads: 2^24 runs at a time
+  const int64_t most = (1 << 24) / nb;   // at least 2^15: K is at most 65536
+  for (int64_t r = 0; r < rows; r += most) {
+    const int64_t runs = (rows - r < most ? rows - r : most) * nb;
+    quantize_kernel<<<dim3(static_cast<unsigned>((runs + 15) / 16)), dim3(256), 0, stream>>>(
+        x + r * K, runs, K, nb, q + r * K, scale + r * scale_row, scale_row, scale_k);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace moe

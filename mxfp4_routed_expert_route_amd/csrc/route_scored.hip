@@ -75,23 +75,31 @@ template <class Logit>
 hipError_t launch_route(const Logit* logits, int64_t T, int E, int k, const ScoreArgs& a,
                         int32_t* ids, float* weights, uint32_t* bm, hipStream_t stream) {
   const int epl = experts_per_lane(a);
-  const dim3 grid(static_cast<unsigned>((T + 3) / 4)), block(256);
-#define MOE_ROUTE(EPL) \
-  route_scored_kernel<EPL><<<grid, block, 0, stream>>>(logits, T, E, k, a, ids, weights, bm)
-  if (epl <= 1)
-    MOE_ROUTE(1);
-  else if (epl <= 2)
-    MOE_ROUTE(2);
-  else if (epl <= 4)
-    MOE_ROUTE(4);
-  else if (epl <= 8)
-    MOE_ROUTE(8);
-  else if (epl <= 16)
-    MOE_ROUTE(16);
-  else
-    MOE_ROUTE(32);
+  const int words = (E + 31) / 32;
+  // a launch has fewer than 2^32 threads: 2^22 tokens at a time
+  for (int64_t at = 0; at < T; at += 1 << 22) {
+    const int64_t n = T - at < (1 << 22) ? T - at : 1 << 22;
+    const dim3 grid(static_cast<unsigned>((n + 3) / 4)), block(256);
+#define MOE_ROUTE(EPL)                                                                         \
+  route_scored_kernel<EPL><<<grid, block, 0, stream>>>(logits + at * E, n, E, k, a, ids + at * k, \
+                                                       weights + at * k, bm ? bm + at * words : bm)
+    if (epl <= 1)
+      MOE_ROUTE(1);
+    else if (epl <= 2)
+      MOE_ROUTE(2);
+    else if (epl <= 4)
+      MOE_ROUTE(4);
+    else if (epl <= 8)
+      MOE_ROUTE(8);
+    else if (epl <= 16)
+      MOE_ROUTE(16);
+    else
+      MOE_ROUTE(32);
 #undef MOE_ROUTE
-  return hipGetLastError();
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 template <class Logit>

@@ -45,7 +45,7 @@ moe_status fp8_workspace_layout(int64_t T, int32_t E, int32_t k, int32_t H, int3
   if (s != MOE_OK) return s;
   const size_t t = static_cast<size_t>(T), slots = t * static_cast<size_t>(k);
   Fp8WsLayout L{};
-  L.tile_rows = fp8_tile_rows(T, E, k);
+  L.tile_rows = fp8_tile_rows(T, E, k, I);
   L.tile_bound = ffn_tile_bound(static_cast<int64_t>(slots), E, L.tile_rows);
   size_t end = 0;
   auto take = [&end](size_t bytes) {

@@ -107,6 +107,28 @@ def test_quantize_zeros_infinities_and_nan():
     assert np.array_equal(q, rq) and np.array_equal(s, rs, equal_nan=True)
 
 
+def test_quantize_more_runs_than_one_launch_takes():
+    from mxfp4_routed_expert_route_amd import binding
+    rows, K = (1 << 23) + 5, 144          # two runs a row; 2^24 runs go into a launch
+    if torch.cuda.mem_get_info()[0] < 10 << 30:
+        pytest.skip("needs 10 GiB")
+    say("quantize", rows, K)
+    rng = np.random.default_rng(5)
+    bits = bf16_rows(rng, 11, K)
+    rq, rs = fp8.quantize_fp8(inputs.bf16_bits_to_f32(bits))
+    n = rows // 11 + 1
+    x = cuda(bits.view(np.int16)).repeat(n, 1)[:rows]
+    q = torch.zeros((rows, K), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((rows, 2), device="cuda")
+    binding.moe_quantize_fp8(x, q, s)
+    torch.cuda.synchronize()
+    for at in (0, (1 << 23) - 11, rows - 11):
+        turn = np.arange(at, at + 11) % 11
+        assert np.array_equal(q[at:at + 11].cpu().numpy(), rq[turn]) and np.array_equal(s[at:at + 11].cpu().numpy(), rs[turn])
+    whole = rows // 11 * 11
+    assert (q[:whole].view(-1, 11, K) == cuda(rq)).all() and (s[:whole].view(-1, 11, 2) == cuda(rs)).all()
+
+
 # ------------------------------------------------------------ dense product
 
 def gpu_gemm(xq, xs, w, ws, f32):
@@ -435,3 +457,20 @@ def test_gemm_beside_other_tensors(m, n, k, f32):
     assert np.isfinite(y).all()
     assert np.array_equal(out[:m].float().cpu().numpy(), y.astype(np.float32))
     assert (out[m:] == 7.0).all()
+
+
+@pytest.mark.parametrize("shape", [(64, 64, 8, 256, 512), (40, 128, 4, 128, 256), (100, 256, 8, 128, 128),
+                                   (18, 2, 2, 256, 128), (9, 256, 8, 128, 512), (640, 64, 2, 128, 512)], ids=str)
+def test_ffn_tiles_for_many_experts(shape):
+    say("ffn", shape)
+    d = ffn_inputs(np.random.default_rng(sum(shape)), *shape)
+    ffn_close(gpu_ffn(d, 10.0), d, 10.0)
+
+
+def test_ffn_all_tokens_to_few_of_many_experts():
+    # 32-row tiles, and experts that fill many of them
+    rng = np.random.default_rng(77)
+    T, E, k = 300, 256, 2
+    ids = np.stack([np.where(np.arange(T) % 9 == 0, 255, 13), np.full(T, 200)], 1)
+    d = ffn_inputs(rng, T, E, k, 128, 128, ids)
+    ffn_close(gpu_ffn(d, 10.0), d, 10.0)

@@ -159,3 +159,24 @@ def test_and_group_equals_the_separate_calls(T, E, k, groups):
         assert np.array_equal(b.gather.cpu().numpy(), gather) and np.array_equal(b.counts.cpu().numpy(), counts)
     else:
         assert (b.counts == 0).all() and (b.offsets == 0).all()
+
+
+def test_more_tokens_than_one_launch_takes():
+    # 2^22 tokens go into a launch; the tokens' experts repeat with period 7
+    from mxfp4_routed_expert_route_amd import binding, layer
+    T, E, k = (1 << 22) + 3, 7, 2
+    print(f"[route_scored] T={T}", file=sys.stderr, flush=True)
+    rows = torch.tensor([[1.0 if (t + 1) % 7 == e else 2.0 if t == e else -e for e in range(7)] for t in range(7)])
+    logits = rows.bfloat16().repeat(T // 7 + 1, 1)[:T].cuda().contiguous()
+    t7 = (torch.arange(T, device="cuda") % 7).int()
+    want = torch.stack([t7, (t7 + 1) % 7], 1).int()
+    b = layer.LayerBuffers.allocate(T, E, k, 128, 128)
+    binding.moe_route_scored_and_group(logits, k, b.topk_ids, b.topk_weights, b.bitmatrix, b.counts, b.offsets,
+                                       b.gather, b.scatter, b.ws, renormalize=True)
+    torch.cuda.synchronize()
+    assert torch.equal(b.topk_ids, want)
+    bits = (1 << want.long()).sum(1)
+    assert torch.equal(b.bitmatrix.view(torch.int32).view(T, -1)[:, 0].long(), bits)
+    assert torch.equal(b.counts.long(), torch.bincount(want.flatten().long(), minlength=E))
+    p = 1 / (1 + np.exp(-1.0))
+    assert (b.topk_weights.double() - torch.tensor([p, 1 - p], dtype=torch.float64, device="cuda")).abs().max() < 1e-6
