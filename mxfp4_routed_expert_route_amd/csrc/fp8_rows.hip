@@ -160,7 +160,8 @@ hipError_t launch(const Fp8Product& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The smallest tile of which the output has at most one per CU; nothing for larger outputs.
+// The smallest tile of which the output has at most one per CU; nothing for larger outputs and,
+// past 16 rows, for a long K (launch_fp8_dense has the figures).
 template <int kOut>
 hipError_t launch_fitting(const Fp8Product& p, hipStream_t stream, bool* done) {
   *done = true;
@@ -168,9 +169,11 @@ hipError_t launch_fitting(const Fp8Product& p, hipStream_t stream, bool* done) {
     return (p.rows + tm - 1) / tm * ((p.n + tn - 1) / tn) <= kFp8Cus;
   };
   if (fits(16, 16)) return launch<1, 1, 8, 2, kOut>(p, stream);
-  if (fits(32, 16)) return launch<2, 1, 8, 2, kOut>(p, stream);
-  if (fits(32, 32)) return launch<2, 2, 8, 2, kOut>(p, stream);
-  if (fits(32, 64)) return launch<2, 4, 8, 1, kOut>(p, stream);
+  // bf16: over a long K the LDS tiles' reads of whole lines are worth their barriers
+  const bool f32 = kOut == kFp8OutF32, tall = f32 || p.K <= 2048, wide = f32 || p.K <= 1024;
+  if (tall && fits(32, 16)) return launch<2, 1, 8, 2, kOut>(p, stream);
+  if (tall && fits(32, 32)) return launch<2, 2, 8, 2, kOut>(p, stream);
+  if (wide && fits(32, 64)) return launch<2, 4, 8, 1, kOut>(p, stream);
   *done = false;
   return hipSuccess;
 }

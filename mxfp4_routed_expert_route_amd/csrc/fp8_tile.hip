@@ -78,19 +78,22 @@ typedef __attribute__((address_space(4))) const float const_float;
 typedef __attribute__((address_space(4))) const int const_int;
 
 constexpr int kXcds = 8;
+constexpr int kFewTiles = 64;
 
 // Nt: streaming shapes, whose weights are read about once: non-temporal copies of them, the
 // column blocks of a tile starting at different runs of K (so that the workgroups of the GPU,
 // which step together, do not all read the same columns of the weights, a few kB apart, at a
 // time: the 512-token burst's first product 684 -> 660 us), and whole-line stores of h.
-template <int TM_, int TN_, int WM_, int WN_, int ST_, bool Nt_>
+// KS: groups of WM x WN wavefronts that take a step's KS runs of K side by side.
+template <int TM_, int TN_, int WM_, int WN_, int ST_, bool Nt_, int KS_ = 1>
 struct Shape {
   static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_;
   static constexpr int ST = ST_;   // steps in LDS
   static constexpr bool Nt = Nt_;
-  static constexpr int NW = WM * WN, threads = 64 * NW;
+  static constexpr int KS = KS_;
+  static constexpr int NW = WM * WN * KS, threads = 64 * NW;
   static constexpr int MT = TM / WM / 16, NF = TN / WN / 16;
-  // 16-byte copies a wavefront issues in a step: activations, then weights.  The rows of
+  // 16-byte copies a wavefront issues for a run: activations, then weights.  The rows of
   // activations may not go round evenly: the first `uneven` wavefronts have one more (0: all
   // have copies_a).
   static constexpr int copies_w = TN / 8 / NW, copies_a = (TM / 8 + NW - 1) / NW, uneven = TM / 8 % NW;
@@ -101,14 +104,14 @@ struct Shape {
   // 256 x 256 tile's step 107 of 690 ns of copies.)
   static constexpr int scale_copies = (TM + 63) / 64 == 3 ? 4 : (TM + 63) / 64, turns = NW / scale_copies;
   static constexpr int w_bytes = TN * 128, a_bytes = TM * 128, s_bytes = scale_copies * 256;
-  static constexpr int a_at = ST * w_bytes, s_at = a_at + ST * a_bytes;
-  static constexpr int red_at = s_at + ST * s_bytes;     // [WN][TM] magnitudes of h's runs
+  static constexpr int slots = ST * KS, a_at = slots * w_bytes, s_at = a_at + slots * a_bytes;
+  static constexpr int red_at = s_at + slots * s_bytes;     // [WN][TM] magnitudes of h's runs
   static constexpr int slots_at = red_at + WN * TM * 4;  // gather entries of the next tile
   static constexpr int h_at = slots_at + s_bytes;        // [TM][128] codes of h
   static constexpr int lds = h_at + (Nt ? TM * 128 : 0);
   static constexpr int per_cu = 160 * 1024 / lds;        // workgroups of a CU
-  static_assert(TM % 16 == 0 && TN % (16 * NW) == 0 && NW % scale_copies == 0 && per_cu >= 1, "shape");
-  static_assert(ST >= 2 && NW % 2 == 0, "copies");
+  static_assert(TM % 16 == 0 && TN % (8 * NW) == 0 && NW % scale_copies == 0 && per_cu >= 1, "shape");
+  static_assert(ST >= 2 && NW % 2 == 0 && (KS == 1 || (NF % 2 == 0 && !Nt)), "copies");
 };
 
 // Workgroups go through (row tile, column block) pairs; the copies run some steps ahead of the
@@ -125,29 +128,36 @@ void tile_kernel(Fp8Product p, int col_blocks) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, g = lane >> 4;
-  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int wm = wave / S::WN % S::WM, wn = wave % S::WN;
+  const int ks = wave / (S::WM * S::WN);   // which of a step's runs it takes
   const int K = p.K, nk = (K + kFp8Block - 1) / kFp8Block;
   // steps past nk copy zeros; SwiGLU's next gather entries need some steps to arrive
   constexpr int kLeast = kSwiglu ? 2 * kAhead : kAhead;
-  const int steps = nk < kLeast ? kLeast : nk;
+  const int all = (nk + S::KS - 1) / S::KS, steps = all < kLeast ? kLeast : all;
   const int half = p.n / 2;
   const int n_blk = (p.n + kFp8Block - 1) / kFp8Block;
   const bool grouped = p.tiles != nullptr;
   const int n_tiles = grouped ? *(const_int*)p.n_tiles : static_cast<int>((p.rows + S::TM - 1) / S::TM);
 
   // Consecutive workgroups go to the XCDs in turn: XCD x takes row tiles x, x + 8, ..., all
-  // column blocks of one from one L2; its workgroups share out the pairs in turn.
+  // column blocks of one from one L2; its workgroups share out the pairs in turn.  With few row
+  // tiles it takes column blocks x, x + 8, ... instead where that spreads the pairs more evenly.
   const int xcd = blockIdx.x % kXcds;
   const int stride = gridDim.x / kXcds;
+  const int most_t = (n_tiles + kXcds - 1) / kXcds * col_blocks;   // the pairs of one XCD
+  const int most_c = (col_blocks + kXcds - 1) / kXcds * n_tiles;
+  const bool by_cols = n_tiles < kFewTiles && (most_c < most_t || (most_c == most_t && !grouped && p.rows < p.n));
   struct Pair {
     int tile, p_begin, expert, rows, n0;   // n0: first output column
     int first;                             // first run of K it takes
   };
   auto pair_at = [&](int local) {
     Pair w;
-    w.tile = (local / col_blocks) * kXcds + xcd;
-    w.n0 = local % col_blocks * (kSwiglu ? S::TN / 2 : S::TN);
-    w.first = S::Nt ? local % col_blocks * nk / col_blocks : 0;
+    const int per = by_cols ? n_tiles : col_blocks, major = local / per * kXcds + xcd, minor = local % per;
+    const int block = by_cols ? major : minor;
+    w.tile = by_cols ? (major < col_blocks ? minor : n_tiles) : major;
+    w.n0 = block * (kSwiglu ? S::TN / 2 : S::TN);
+    w.first = S::Nt ? block * nk / col_blocks : 0;
     w.expert = 0;
     w.rows = 0;
     w.p_begin = 0;
@@ -220,17 +230,17 @@ void tile_kernel(Fp8Product p, int col_blocks) {
     soff = srow < 0 ? kRsrcOutOfRange : static_cast<uint32_t>(srow) * static_cast<uint32_t>(p.scale_row) * 4u;
     w_first = a_first = w.first;
   };
-  auto run_of = [&](int kb, int first) {   // run of K that step kb takes; past the last: any
+  auto run_of = [&](int kb, int first) {   // kb-th run of K; past the last: any
     return kb >= nk ? 0 : S::Nt && kb + first >= nk ? kb + first - nk : kb + first;
   };
   const int short_run = K % kFp8Block ? nk - 1 : -1;   // the run that ends early
-  // step kb's scales, if it is this wavefront's turn
+  // run kb's scales, if it is this wavefront's turn
   auto copy_s = [&](int kb, int slot) {
     if (static_cast<int>(static_cast<unsigned>(kb) % S::turns) == wave / S::scale_copies)   // uniform
       copy4(srs, soff, static_cast<uint32_t>(run_of(kb, a_first)) * static_cast<uint32_t>(p.scale_k) * 4u,
             lds0 + S::s_at + slot * S::s_bytes + 256 * (wave % S::scale_copies));
   };
-  // copy c of step kb's activations.  Past the last run they are not zeros, but the weights are.
+  // copy c of run kb's activations.  Past the last run they are not zeros, but the weights are.
   auto copy_a = [&](int c, int kb, int slot) {
     if (c + 1 == S::copies_a && a_short) return;   // uniform
     const int run = run_of(kb, a_first);
@@ -239,7 +249,7 @@ void tile_kernel(Fp8Product p, int col_blocks) {
     if (run == short_run) v = static_cast<int>(k0 + c_piece) < K ? v : kRsrcOutOfRange;   // zeros past K
     copy16<false>(ars, v, k0, lds0 + S::a_at + slot * S::a_bytes + 1024 * (wave + S::NW * c));
   };
-  // copy c of step kb's weights; zeros past the last run
+  // copy c of run kb's weights; zeros past the last run
   auto copy_w = [&](int c, int kb, int slot) {
     const int run = run_of(kb, w_first);
     const uint32_t k0 = static_cast<uint32_t>(run) * 128u;
@@ -248,22 +258,23 @@ void tile_kernel(Fp8Product p, int col_blocks) {
     if (run == short_run) v = static_cast<int>(k0 + c_piece) < K ? v : kRsrcOutOfRange;
     copy16<S::Nt>(wrs, v, k0, lds0 + slot * S::w_bytes + 1024 * (wave + S::NW * c));
   };
-  constexpr int kCopies = 1 + S::copies_a + S::copies_w;
-  auto copy_part = [&](int c, int kb, int slot) {
+  constexpr int kRun = 1 + S::copies_a + S::copies_w, kCopies = S::KS * kRun;
+  auto copy_part = [&](int part, int step, int slot) {
+    const int c = part % kRun, kb = step * S::KS + part / kRun, at = slot * S::KS + part / kRun;
     if (c == 0)
-      copy_s(kb, slot);
+      copy_s(kb, at);
     else if (c <= S::copies_a)
-      copy_a(c - 1, kb, slot);
+      copy_a(c - 1, kb, at);
     else
-      copy_w(c - 1 - S::copies_a, kb, slot);
+      copy_w(c - 1 - S::copies_a, kb, at);
   };
   // waits until only copies on their way for later steps are left, and `more` steps' besides
   auto wait_step = [&](auto more) {
     constexpr int n = S::ST - 2 + decltype(more)::value;
     if (a_short)   // uniform
-      wait_copies<n * (S::copies_a - 1 + S::copies_w)>();
+      wait_copies<n * S::KS * (S::copies_a - 1 + S::copies_w)>();
     else
-      wait_copies<n * (S::copies_a + S::copies_w)>();
+      wait_copies<n * S::KS * (S::copies_a + S::copies_w)>();
   };
   aim(cur, std::true_type{});
 #pragma unroll
@@ -278,8 +289,9 @@ void tile_kernel(Fp8Product p, int col_blocks) {
     const i32x4 hi = *reinterpret_cast<const i32x4*>(base + row0 * 128 + (place ^ 64));
     return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   };
-  const unsigned char* part = tile_lds + S::a_at + wm * (S::TM / S::WM) * 128;
-  const unsigned char* xpart = tile_lds + S::s_at + (wm * (S::TM / S::WM) + r16) * 4;
+  const unsigned char* wpart = tile_lds + ks * S::w_bytes;
+  const unsigned char* part = tile_lds + S::a_at + ks * S::a_bytes + wm * (S::TM / S::WM) * 128;
+  const unsigned char* xpart = tile_lds + S::s_at + ks * S::s_bytes + (wm * (S::TM / S::WM) + r16) * 4;
   int slot = 0, fill = kAhead % S::ST;
   for (;;) {
     local += stride;
@@ -311,6 +323,8 @@ void tile_kernel(Fp8Product p, int col_blocks) {
     // this one's as the last MFMAs take them, and the slot is filled again during the next
     // step, a few copies a fragment (all at once, the wavefronts would stand at the full copy
     // queue instead of multiplying).
+    constexpr bool kPast = !kSwiglu && (S::KS > 1 || kAhead > 1);
+    constexpr bool kStops = MT * NF <= 24;   // (the largest tile has no registers left for branches)
     auto loop = [&](auto frags) {
       constexpr int NS = decltype(frags)::value;
       wait_step(std::integral_constant<int, kLate ? 0 : 1>{});
@@ -324,26 +338,30 @@ void tile_kernel(Fp8Product p, int col_blocks) {
               lds0 + S::slots_at + 256 * wave);
       }
       i32x8 a[NF], b{};
-      float x = 0.f, w0 = ws0[cur.first], w1 = ws1[cur.first];
+      const int first = S::KS == 1 ? cur.first : ks < nk ? ks : 0;
+      float x = 0.f, w0 = ws0[first], w1 = ws1[first];
       if constexpr (NS > 0) {
 #pragma unroll
-        for (int f = 0; f < NF; ++f) a[f] = read_frag(tile_lds + slot * S::w_bytes, wn * NR + 16 * f);
-        b = read_frag(part + slot * S::a_bytes, 0);
-        x = *reinterpret_cast<const float*>(xpart + slot * S::s_bytes);
+        for (int f = 0; f < NF; ++f) a[f] = read_frag(wpart + slot * S::KS * S::w_bytes, wn * NR + 16 * f);
+        b = read_frag(part + slot * S::KS * S::a_bytes, 0);
+        x = *reinterpret_cast<const float*>(xpart + slot * S::KS * S::s_bytes);
       }
       // the copies of this pair's steps, then of the next pair's first ones
       int kb = 0, ahead = kAhead;
+      bool copying = true;
 #pragma unroll 1
       for (int lap = 0; lap < 2; ++lap) {
         const int end = lap == 0 ? steps - kAhead : steps;
         if (lap == 1) {
+          copying = more || !kStops;
           ahead = more ? kAhead - steps : 1 << 20;   // no step: zeros
           if (more) aim(nxt, std::false_type{});
         }
 #pragma unroll 1
         for (; kb < end; ++kb) {
           const int next = slot + 1 == S::ST ? 0 : slot + 1;
-          int kn = kb + 1 < nk ? kb + 1 + cur.first : 0;
+          int kn = (kb + 1) * S::KS + ks;   // its next run
+          kn = kn < nk ? kn + cur.first : 0;
           if (S::Nt && kn >= nk) kn -= nk;
           const float w0n = ws0[kn], w1n = kSwiglu ? ws1[kn] : w0n;
           floatx4 d[NF];
@@ -357,7 +375,7 @@ void tile_kernel(Fp8Product p, int col_blocks) {
             // stand meanwhile), unless the step has no other fragment before its wait.
             constexpr bool kAfter = kLate && NS >= 2 && MT * NF <= 16;
             constexpr int kOver = NS >= 4 ? NS / 2 : 1, kEach = (kCopies + kOver - 1) / kOver;
-            if (kLate && !kAfter) {
+            if (kLate && !kAfter && (!kStops || copying)) {   // uniform
 #pragma unroll
               for (int c = 0; c < kCopies; ++c)
                 if (c / kEach == m) copy_part(c, kb + ahead, fill);
@@ -365,13 +383,17 @@ void tile_kernel(Fp8Product p, int col_blocks) {
             i32x8 b_next = b;
             float x_next = x;
             if (!last) {
-              b_next = read_frag(part + slot * S::a_bytes, 16 * (m + 1));
-              x_next = *reinterpret_cast<const float*>(xpart + slot * S::s_bytes + 64 * (m + 1));
+              b_next = read_frag(part + slot * S::KS * S::a_bytes, 16 * (m + 1));
+              x_next = *reinterpret_cast<const float*>(xpart + slot * S::KS * S::s_bytes + 64 * (m + 1));
             } else {
               wait_lds();
-              wait_step(std::integral_constant<int, 0>{});   // this wavefront's copies of the next step
+              // this wavefront's copies of the next step; none behind them: all
+              if (!kStops || copying)
+                wait_step(std::integral_constant<int, 0>{});
+              else
+                wait_copies<0>();
               barrier();                                     // everybody's; and this step has been read
-              if (!kLate) {
+              if (!kLate && (!kStops || copying)) {
 #pragma unroll
                 for (int c = 0; c < kCopies; ++c) copy_part(c, kb + ahead, fill);
               }
@@ -382,11 +404,13 @@ void tile_kernel(Fp8Product p, int col_blocks) {
                 for (int f = 0; f < NF; ++f) asm volatile("" : "+v"(d[f]));
               }
               floatx4 dn[NF];
-              const float t0 = x * w0, t1 = kSwiglu ? x * w1 : t0;
+              // past the last run the weights are zeros, the scales any (grouped: none infinite)
+              const bool run = !kPast || kb * S::KS + ks < nk;
+              const float t0 = run ? x * w0 : 0.f, t1 = kSwiglu ? (run ? x * w1 : 0.f) : t0;
 #pragma unroll
               for (int f = 0; f < NF; ++f) {
                 dn[f] = mfma_e4m3<kFull>(a[f], b);
-                if (last) a[f] = read_frag(tile_lds + next * S::w_bytes, wn * NR + 16 * f);
+                if (last) a[f] = read_frag(wpart + next * S::KS * S::w_bytes, wn * NR + 16 * f);
                 if (m > 0) {
                   const float s = f < NF / 2 ? s0 : s1;
 #pragma unroll
@@ -394,10 +418,10 @@ void tile_kernel(Fp8Product p, int col_blocks) {
                 }
               }
               if (last) {
-                b_next = read_frag(part + next * S::a_bytes, 0);
-                x_next = *reinterpret_cast<const float*>(xpart + next * S::s_bytes);
+                b_next = read_frag(part + next * S::KS * S::a_bytes, 0);
+                x_next = *reinterpret_cast<const float*>(xpart + next * S::KS * S::s_bytes);
               }
-              if (kAfter && m == 0) {
+              if (kAfter && m == 0 && (!kStops || copying)) {
                 __builtin_amdgcn_sched_barrier(0);   // the MFMAs first
 #pragma unroll
                 for (int c = 0; c < kCopies; ++c) copy_part(c, kb + ahead, fill);
@@ -446,6 +470,34 @@ void tile_kernel(Fp8Product p, int col_blocks) {
       loop(std::integral_constant<int, MT < 4 ? MT : 4>{});
     else
       loop(std::integral_constant<int, MT>{});
+
+    // the groups' sums, added in the groups' order: each group finishes every KS-th pair of
+    // weight fragments
+    auto mine = [&](int m, int f) { return S::KS == 1 || (m * (NF / 2) + f / 2) % S::KS == ks; };
+    if constexpr (S::KS > 1) {
+      static_assert(S::NW * MT * NF * 1024 <= S::s_at, "in the steps' LDS");
+      floatx4* sums = reinterpret_cast<floatx4*>(tile_lds) + wave % (S::WM * S::WN) * (MT * NF * 64) + lane;
+      constexpr int kGroup = S::WM * S::WN * MT * NF * 64;
+      wait_copies<0>();
+      wait_lds();
+      barrier();   // no copy and no read of the steps' LDS is left: this was the only pair
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int f = 0; f < NF; ++f) sums[ks * kGroup + (m * NF + f) * 64] = acc[m][f];
+      wait_lds();
+      barrier();
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+          if (mine(m, f)) {
+            floatx4 s = sums[(m * NF + f) * 64];
+#pragma unroll
+            for (int o = 1; o < S::KS; ++o) s += sums[o * kGroup + (m * NF + f) * 64];
+            acc[m][f] = s;
+          }
+    }
 
     // ---- results: lane has rows wm part + 16 m + r16, 4 NF (SwiGLU 2 NF) consecutive columns
     if constexpr (kSwiglu) {
@@ -529,6 +581,7 @@ void tile_kernel(Fp8Product p, int col_blocks) {
         const int64_t at = (p_begin + r) * p.ld_out;
 #pragma unroll
         for (int f = 0; f < NF; f += 2) {
+          if (!mine(m, f)) continue;
           const int c = c0 + 16 * f;
           if (wide && c < p.n) {
             if constexpr (kOut == kFp8OutF32) {
@@ -567,12 +620,14 @@ hipError_t launch(const Fp8Product& p, hipStream_t stream) {
   const int per = kOut == kFp8OutSwiglu ? S::TN / 2 : S::TN;
   const int col_blocks = (cols + per - 1) / per;
   const int64_t tiles = p.tiles ? p.tile_bound : (p.rows + S::TM - 1) / S::TM;
-  const int64_t pairs = (tiles + kXcds - 1) / kXcds * kXcds * col_blocks;
+  // either way of giving pairs to XCDs; with KS > 1 (outputs of few tiles) a workgroup takes one
+  const int64_t by_tiles = (tiles + kXcds - 1) / kXcds * col_blocks, by_cols = (col_blocks + kXcds - 1) / kXcds * tiles;
+  const int64_t pairs = kXcds * (by_tiles > by_cols ? by_tiles : by_cols);
   const int64_t most = static_cast<int64_t>(kFp8Cus) * S::per_cu;
   static const hipError_t attr = hipFuncSetAttribute(
       reinterpret_cast<const void*>(tile_kernel<S, kOut>), hipFuncAttributeMaxDynamicSharedMemorySize, S::lds);
   if (attr != hipSuccess) return attr;
-  tile_kernel<S, kOut><<<dim3(static_cast<unsigned>(pairs < most ? pairs : most)), dim3(S::threads), S::lds,
+  tile_kernel<S, kOut><<<dim3(static_cast<unsigned>(pairs < most || S::KS > 1 ? pairs : most)), dim3(S::threads), S::lds,
                          stream>>>(p, col_blocks);
   return hipGetLastError();
 }
@@ -594,11 +649,21 @@ hipError_t launch_fp8_grouped(int tile_rows, const Fp8Product& p, hipStream_t st
                                      : launch_grouped<kFp8OutBf16>(tile_rows, p, stream);
 }
 
+// The smallest tile of which the output has at most one per CU (fp8_rows.hip has the smallest).
+// Small tiles are bound by what a step costs beside its products, so K is shared out as well.
+// Measured (us in a graph; the 32 x 64 tile with K in 4 / the rows kernel's / the 64 x 128 tile):
+// 128x4096x4096 11.5 / 15.9 / 18.2, 128x4096x2048 8.2 / 9.7 / 11.2; the 32 x 32 tile with K in 4 /
+// the rows kernel's: 256x1024x4096 8.6 / 11.8, 64x4096x4096 10.1 / 12.0; the 64 x 64 tile with K
+// in 2 / the 64 x 128 tile: 256x4096x4096 15.5 / 18.2, 256x4096x2048 10.4 / 11.2.  The 64 x 128
+// tile gains nothing from K in 2 (512 rows: K = 4096 18.0 / 18.5, 2048 11.7 / 11.4, 1024 8.6 / 7.8).
 hipError_t launch_fp8_dense(const Fp8Product& p, hipStream_t stream) {
   if (p.out_kind == kFp8OutF32) return launch<Shape<64, 128, 1, 4, 3, false>, kFp8OutF32>(p, stream);
   auto fits = [&](int tm, int tn) {
     return (p.rows + tm - 1) / tm * ((p.n + tn - 1) / tn) <= kFp8Cus;
   };
+  if (fits(32, 32)) return launch<Shape<32, 32, 1, 1, 4, false, 4>, kFp8OutBf16>(p, stream);
+  if (fits(32, 64)) return launch<Shape<32, 64, 1, 1, 3, false, 4>, kFp8OutBf16>(p, stream);
+  if (fits(64, 64)) return launch<Shape<64, 64, 1, 2, 3, false, 2>, kFp8OutBf16>(p, stream);
   if (fits(64, 128)) return launch<Shape<64, 128, 2, 2, 3, false>, kFp8OutBf16>(p, stream);
   if (fits(128, 128)) return launch<Shape<128, 128, 2, 4, 4, false>, kFp8OutBf16>(p, stream);
   if (fits(128, 256)) return launch<Shape<128, 256, 2, 4, 3, false>, kFp8OutBf16>(p, stream);

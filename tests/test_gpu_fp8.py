@@ -474,3 +474,29 @@ def test_ffn_all_tokens_to_few_of_many_experts():
     ids = np.stack([np.where(np.arange(T) % 9 == 0, 255, 13), np.full(T, 200)], 1)
     d = ffn_inputs(rng, T, E, k, 128, 128, ids)
     ffn_close(gpu_ffn(d, 10.0), d, 10.0)
+
+
+@pytest.mark.parametrize("M,N,K", [(65, 1100, 2064), (40, 2000, 2176), (129, 3000, 1040), (250, 2041, 1152), (300, 2500, 400),
+                                   (260, 2561, 272), (500, 3000, 272), (700, 4100, 144), (1500, 4200, 128),
+                                   (2050, 4100, 128), (2305, 4097, 272), (70, 33000, 128), (17, 70000, 144)])
+def test_gemm_every_tile(M, N, K):
+    say("gemm", M, N, K)
+    rng = np.random.default_rng(M + N + K)
+    xq, w = codes(rng, M, K), codes(rng, N, K)
+    xs, ws = scales(rng, M, -(-K // 128)), scales(rng, -(-N // 128), -(-K // 128))
+    gemm_close(gpu_gemm(xq, xs, w, ws, False), xq, xs, w, ws, False)
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 40, 144), (65, 1100, 2192), (129, 3000, 1040), (300, 2500, 144), (500, 3000, 272),
+                                   (700, 4100, 144), (1500, 4200, 128)])
+@pytest.mark.parametrize("f32", [True, False])
+def test_gemm_infinite_scale_stays_in_its_row(M, N, K, f32):
+    # codes above zero: an infinite scale's row is infinite, whatever stands beside its last run
+    say("gemm inf", M, N, K, f32)
+    rng = np.random.default_rng(M)
+    xq, w = rng.integers(1, 0x7F, (M, K)).astype(np.uint8), rng.integers(1, 0x7F, (N, K)).astype(np.uint8)
+    xs, ws = scales(rng, M, -(-K // 128)), scales(rng, -(-N // 128), -(-K // 128))
+    xs[3, 0] = np.inf
+    y = gpu_gemm(xq, xs, w, ws, f32)
+    assert (y[3] == np.inf).all()
+    assert np.isfinite(np.delete(y, 3, 0)).all()
