@@ -169,8 +169,8 @@ hipError_t launch_fitting(const Fp8Product& p, hipStream_t stream, bool* done) {
     return (p.rows + tm - 1) / tm * ((p.n + tn - 1) / tn) <= kFp8Cus;
   };
   if (fits(16, 16)) return launch<1, 1, 8, 2, kOut>(p, stream);
-  // bf16: over a long K the LDS tiles' reads of whole lines are worth their barriers
-  const bool f32 = kOut == kFp8OutF32, tall = f32 || p.K <= 2048, wide = f32 || p.K <= 1024;
+  // over a long K the LDS tiles' reads of whole lines are worth their barriers
+  const bool tall = p.K <= 2048, wide = p.K <= 1024;
   if (tall && fits(32, 16)) return launch<2, 1, 8, 2, kOut>(p, stream);
   if (tall && fits(32, 32)) return launch<2, 2, 8, 2, kOut>(p, stream);
   if (wide && fits(32, 64)) return launch<2, 4, 8, 1, kOut>(p, stream);

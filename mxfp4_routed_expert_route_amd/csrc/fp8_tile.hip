@@ -642,13 +642,6 @@ hipError_t launch_grouped(int tile_rows, const Fp8Product& p, hipStream_t stream
   return launch<Shape<256, 256, 2, 4, 2, false>, kOut>(p, stream);
 }
 
-}  // namespace
-
-hipError_t launch_fp8_grouped(int tile_rows, const Fp8Product& p, hipStream_t stream) {
-  return p.out_kind == kFp8OutSwiglu ? launch_grouped<kFp8OutSwiglu>(tile_rows, p, stream)
-                                     : launch_grouped<kFp8OutBf16>(tile_rows, p, stream);
-}
-
 // The smallest tile of which the output has at most one per CU (fp8_rows.hip has the smallest).
 // Small tiles are bound by what a step costs beside its products, so K is shared out as well.
 // Measured (us in a graph; the 32 x 64 tile with K in 4 / the rows kernel's / the 64 x 128 tile):
@@ -656,18 +649,31 @@ hipError_t launch_fp8_grouped(int tile_rows, const Fp8Product& p, hipStream_t st
 // the rows kernel's: 256x1024x4096 8.6 / 11.8, 64x4096x4096 10.1 / 12.0; the 64 x 64 tile with K
 // in 2 / the 64 x 128 tile: 256x4096x4096 15.5 / 18.2, 256x4096x2048 10.4 / 11.2.  The 64 x 128
 // tile gains nothing from K in 2 (512 rows: K = 4096 18.0 / 18.5, 2048 11.7 / 11.4, 1024 8.6 / 7.8).
-hipError_t launch_fp8_dense(const Fp8Product& p, hipStream_t stream) {
-  if (p.out_kind == kFp8OutF32) return launch<Shape<64, 128, 1, 4, 3, false>, kFp8OutF32>(p, stream);
+// fp32 results, whose products are bf16 MFMAs on converted operands, take the same tiles but the
+// largest (registers); 4096x4096x4096: 130 us with 128 x 256, 172 with 64 x 128.
+template <int kOut>
+hipError_t launch_dense(const Fp8Product& p, hipStream_t stream) {
   auto fits = [&](int tm, int tn) {
     return (p.rows + tm - 1) / tm * ((p.n + tn - 1) / tn) <= kFp8Cus;
   };
-  if (fits(32, 32)) return launch<Shape<32, 32, 1, 1, 4, false, 4>, kFp8OutBf16>(p, stream);
-  if (fits(32, 64)) return launch<Shape<32, 64, 1, 1, 3, false, 4>, kFp8OutBf16>(p, stream);
-  if (fits(64, 64)) return launch<Shape<64, 64, 1, 2, 3, false, 2>, kFp8OutBf16>(p, stream);
-  if (fits(64, 128)) return launch<Shape<64, 128, 2, 2, 3, false>, kFp8OutBf16>(p, stream);
-  if (fits(128, 128)) return launch<Shape<128, 128, 2, 4, 4, false>, kFp8OutBf16>(p, stream);
-  if (fits(128, 256)) return launch<Shape<128, 256, 2, 4, 3, false>, kFp8OutBf16>(p, stream);
-  return launch<Shape<256, 256, 2, 4, 2, false>, kFp8OutBf16>(p, stream);
+  if (fits(32, 32)) return launch<Shape<32, 32, 1, 1, 4, false, 4>, kOut>(p, stream);
+  if (fits(32, 64)) return launch<Shape<32, 64, 1, 1, 3, false, 4>, kOut>(p, stream);
+  if (fits(64, 64)) return launch<Shape<64, 64, 1, 2, 3, false, 2>, kOut>(p, stream);
+  if (fits(64, 128)) return launch<Shape<64, 128, 2, 2, 3, false>, kOut>(p, stream);
+  if (fits(128, 128)) return launch<Shape<128, 128, 2, 4, 4, false>, kOut>(p, stream);
+  if (kOut == kFp8OutF32 || fits(128, 256)) return launch<Shape<128, 256, 2, 4, 3, false>, kOut>(p, stream);
+  if constexpr (kOut == kFp8OutBf16) return launch<Shape<256, 256, 2, 4, 2, false>, kOut>(p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_fp8_grouped(int tile_rows, const Fp8Product& p, hipStream_t stream) {
+  return p.out_kind == kFp8OutSwiglu ? launch_grouped<kFp8OutSwiglu>(tile_rows, p, stream)
+                                     : launch_grouped<kFp8OutBf16>(tile_rows, p, stream);
+}
+
+hipError_t launch_fp8_dense(const Fp8Product& p, hipStream_t stream) {
+  return p.out_kind == kFp8OutF32 ? launch_dense<kFp8OutF32>(p, stream) : launch_dense<kFp8OutBf16>(p, stream);
 }
 
 }  // namespace moe

@@ -479,12 +479,13 @@ def test_ffn_all_tokens_to_few_of_many_experts():
 @pytest.mark.parametrize("M,N,K", [(65, 1100, 2064), (40, 2000, 2176), (129, 3000, 1040), (250, 2041, 1152), (300, 2500, 400),
                                    (260, 2561, 272), (500, 3000, 272), (700, 4100, 144), (1500, 4200, 128),
                                    (2050, 4100, 128), (2305, 4097, 272), (70, 33000, 128), (17, 70000, 144)])
-def test_gemm_every_tile(M, N, K):
-    say("gemm", M, N, K)
+@pytest.mark.parametrize("f32", [True, False])
+def test_gemm_every_tile(M, N, K, f32):
+    say("gemm", M, N, K, f32)
     rng = np.random.default_rng(M + N + K)
     xq, w = codes(rng, M, K), codes(rng, N, K)
     xs, ws = scales(rng, M, -(-K // 128)), scales(rng, -(-N // 128), -(-K // 128))
-    gemm_close(gpu_gemm(xq, xs, w, ws, False), xq, xs, w, ws, False)
+    gemm_close(gpu_gemm(xq, xs, w, ws, f32), xq, xs, w, ws, f32)
 
 
 @pytest.mark.parametrize("M,N,K", [(5, 40, 144), (65, 1100, 2192), (129, 3000, 1040), (300, 2500, 144), (500, 3000, 272),
