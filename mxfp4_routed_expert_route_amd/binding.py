@@ -278,38 +278,44 @@ LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
 FP8_BLOCK = 128
 
 
+_F32, _I32, _U8 = (torch.float32,), (torch.int32,), (torch.uint8,)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_several = None   # more than one GPU is visible
+_fns = {}
 
 
-def _arg(t, dtype, shape, dev, name):
+def _arg(t, dtypes, shape, dev, name):
     """Pointer of a tensor on GPU `dev`, checked: dtype, shape, contiguity.  The checks cost
-    about as much as the call's own launch, so there is one pass over a tensor's properties."""
-    if t.dtype is not dtype and not (dtype.__class__ is tuple and t.dtype in dtype):
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev or dev < 0:
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a GPU tensor")
+    about as much as the call's own launch, so a right tensor passes in one expression."""
+    if t is not None and t.dtype in dtypes and t.shape == shape and t.get_device() == dev >= 0 and t.is_contiguous():
+        return t.data_ptr()
+    if t is None or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {None if t is None else t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on another GPU than the other tensors")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _ws(t, dev):
-    return (None, 0) if t is None else (_arg(t, torch.uint8, t.shape, dev, "ws"), t.numel())
+    return (None, 0) if t is None else (_arg(t, _U8, t.shape, dev, "ws"), t.numel())
 
 
 def _run(fn: str, dev: int, stream, *args):
     """Calls entry point `fn` on `dev`'s current stream, or the stream given."""
+    global _several
     if stream is None:
         handle = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
     else:
         handle = _stream(stream)
-    call = getattr(_lib or load(), fn)
-    if dev == (_current_device() if _current_device else torch.cuda.current_device()):
+    call = _fns.get(fn)
+    if call is None:
+        call = _fns[fn] = getattr(load(), fn)
+        _several = torch.cuda.device_count() > 1
+    if not _several or dev == torch.cuda.current_device():
         code = call(*args, handle)
     else:
         with torch.cuda.device(dev):
@@ -333,11 +339,11 @@ def _scored(logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups,
     if kind is None:
         raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     dev = logits.get_device()
-    return (_arg(logits, logits.dtype, (T, E), dev, "logits"), kind, T, E, k, SCORES[score],
-            None if bias is None else _arg(bias, torch.float32, (E,), dev, "bias"),
+    return (_arg(logits, LOGIT_TYPES, (T, E), dev, "logits"), kind, T, E, k, SCORES[score],
+            None if bias is None else _arg(bias, _F32, (E,), dev, "bias"),
             groups, topk_groups, group_top, 1 if renormalize else 0, scale,
-            _arg(topk_ids, torch.int32, (T, k), dev, "topk_ids"),
-            _arg(topk_weights, torch.float32, (T, k), dev, "topk_weights"))
+            _arg(topk_ids, _I32, (T, k), dev, "topk_ids"),
+            _arg(topk_weights, _F32, (T, k), dev, "topk_weights"))
 
 
 def moe_route_scored(logits, k: int, topk_ids, topk_weights, *, score: str = "softmax", bias=None,
@@ -358,11 +364,11 @@ def moe_route_scored_and_group(logits, k: int, topk_ids, topk_weights, bitmatrix
     how = _scored(logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups, group_top,
                   renormalize, scale)
     T, E = logits.shape
-    dev, i32 = logits.get_device(), torch.int32
+    dev = logits.get_device()
     _run("moe_route_scored_and_group", dev, stream, *how,
-         _arg(bitmatrix, i32, (T, (E + 31) // 32), dev, "bitmatrix"),
-         _arg(counts, i32, (E,), dev, "counts"), _arg(offsets, i32, (E + 1,), dev, "offsets"),
-         _arg(gather, i32, (T * k,), dev, "gather"), _arg(scatter, i32, (T * k,), dev, "scatter"),
+         _arg(bitmatrix, _I32, (T, (E + 31) // 32), dev, "bitmatrix"),
+         _arg(counts, _I32, (E,), dev, "counts"), _arg(offsets, _I32, (E + 1,), dev, "offsets"),
+         _arg(gather, _I32, (T * k,), dev, "gather"), _arg(scatter, _I32, (T * k,), dev, "scatter"),
          *_ws(ws, dev))
 
 
@@ -374,7 +380,7 @@ def moe_quantize_fp8(x, q, scale, stream=None):
     dev = x.get_device()
     _run("moe_quantize_fp8", dev, stream, _arg(x, BF16, (rows, K), dev, "x"), rows, K,
          _arg(q, E4M3, (rows, K), dev, "q"),
-         _arg(scale, torch.float32, (rows, _runs(K)), dev, "scale"))
+         _arg(scale, _F32, (rows, _runs(K)), dev, "scale"))
 
 
 def moe_gemm_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
@@ -388,12 +394,12 @@ def moe_gemm_fp8(xq, x_scale, w, w_scale, y, ws=None, stream=None):
         raise ValueError("xq must be [M, K] and w [N, K]")
     M, K = xq.shape
     N = w.shape[0]
-    dev, f32 = xq.get_device(), torch.float32
-    kind = 0 if y.dtype is f32 else 1
+    dev, nk = xq.get_device(), _runs(K)
+    kind = 0 if y.dtype is torch.float32 else 1
     _run("moe_gemm_fp8", dev, stream, _arg(xq, E4M3, (M, K), dev, "xq"),
-         _arg(x_scale, f32, (M, _runs(K)), dev, "x_scale"), M, N, K,
-         _arg(w, E4M3, (N, K), dev, "w"), _arg(w_scale, f32, (_runs(N), _runs(K)), dev, "w_scale"),
-         kind, _arg(y, BF16 if kind else f32, (M, N), dev, "y"), *_ws(ws, dev))
+         _arg(x_scale, _F32, (M, nk), dev, "x_scale"), M, N, K,
+         _arg(w, E4M3, (N, K), dev, "w"), _arg(w_scale, _F32, (_runs(N), nk), dev, "w_scale"),
+         kind, _arg(y, BF16 if kind else _F32, (M, N), dev, "y"), *_ws(ws, dev))
 
 
 def moe_fp8_workspace_bytes(T: int, E: int, k: int, H: int, I: int) -> int:
@@ -408,12 +414,12 @@ def moe_grouped_ffn_fp8(x, k: int, w1, w1_scale, w2, w2_scale, counts, offsets, 
         raise ValueError("x must be [T, H] and w1 [E, 2I, H]")
     T, H = x.shape
     E, I = w1.shape[0], w1.shape[1] // 2
-    dev, f32, i32 = x.get_device(), torch.float32, torch.int32
+    dev = x.get_device()
     _run("moe_grouped_ffn_fp8", dev, stream, _arg(x, BF16, (T, H), dev, "x"), T, H, I, E, k,
          _arg(w1, E4M3, (E, 2 * I, H), dev, "w1"),
-         _arg(w1_scale, f32, (E, _runs(2 * I), _runs(H)), dev, "w1_scale"),
+         _arg(w1_scale, _F32, (E, _runs(2 * I), _runs(H)), dev, "w1_scale"),
          _arg(w2, E4M3, (E, H, I), dev, "w2"),
-         _arg(w2_scale, f32, (E, _runs(H), _runs(I)), dev, "w2_scale"),
-         _arg(counts, i32, (E,), dev, "counts"), _arg(offsets, i32, (E + 1,), dev, "offsets"),
-         _arg(gather, i32, (T * k,), dev, "gather"), swiglu_limit,
+         _arg(w2_scale, _F32, (E, _runs(H), _runs(I)), dev, "w2_scale"),
+         _arg(counts, _I32, (E,), dev, "counts"), _arg(offsets, _I32, (E + 1,), dev, "offsets"),
+         _arg(gather, _I32, (T * k,), dev, "gather"), swiglu_limit,
          _arg(y_sorted, BF16, (T * k, H), dev, "y_sorted"), *_ws(ws, dev))

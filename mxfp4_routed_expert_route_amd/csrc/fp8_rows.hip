@@ -160,18 +160,19 @@ hipError_t launch(const Fp8Product& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// The smallest tile of which the output has at most one per CU; nothing for larger outputs and,
-// past 16 rows, for a long K (launch_fp8_dense has the figures).
+// The smallest tile of which the output has at most one per CU; nothing for larger outputs and
+// for a long K.  Over a long K the LDS tiles' reads of whole lines are worth their barriers
+// (launch_fp8_dense has the figures), but not against 32 x 16 tiles that leave CUs idle: this
+// kernel / the 32 x 32 LDS tile, us, K = 4096: 64x1024 (128 tiles) 7.0 / 8.5, 128x1024 (256) 9.8 / 8.5.
 template <int kOut>
 hipError_t launch_fitting(const Fp8Product& p, hipStream_t stream, bool* done) {
   *done = true;
-  auto fits = [&](int tm, int tn) {
-    return (p.rows + tm - 1) / tm * ((p.n + tn - 1) / tn) <= kFp8Cus;
+  auto fits = [&](int tm, int tn, int most = kFp8Cus) {
+    return (p.rows + tm - 1) / tm * ((p.n + tn - 1) / tn) <= most;
   };
   if (fits(16, 16)) return launch<1, 1, 8, 2, kOut>(p, stream);
-  // over a long K the LDS tiles' reads of whole lines are worth their barriers
   const bool tall = p.K <= 2048, wide = p.K <= 1024;
-  if (tall && fits(32, 16)) return launch<2, 1, 8, 2, kOut>(p, stream);
+  if (fits(32, 16, tall ? kFp8Cus : kFp8Cus * 3 / 4)) return launch<2, 1, 8, 2, kOut>(p, stream);
   if (tall && fits(32, 32)) return launch<2, 2, 8, 2, kOut>(p, stream);
   if (wide && fits(32, 64)) return launch<2, 4, 8, 1, kOut>(p, stream);
   *done = false;
