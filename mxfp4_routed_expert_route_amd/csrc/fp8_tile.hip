@@ -1,8 +1,9 @@
 // Block-scaled FP8 product on LDS tiles: TM activation rows x TN weight rows a workgroup.
 //
-// K goes in steps of one run (128 elements, 128 bytes a row).  A step's weight and
+// K goes in steps of one run (128 elements, 128 bytes a row; KS groups of wavefronts: of KS
+// runs, one each, their sums added at the end).  A step's weight and
 // activation rows and activation scales are copied to LDS by buffer loads that write LDS
-// themselves, kStages steps deep, one barrier a step.  The wavefronts share the tile as
+// themselves, ST steps deep, one barrier a step.  A group's wavefronts share the tile as
 // WM x WN; a wavefront's part is MT 16-row activation fragments by NF 16-row weight
 // fragments.  Weights are the MFMA's A operand, so a lane of D holds four weight rows
 // (output columns) of one activation row, and one multiplier, x_scale * w_scale, serves
@@ -18,6 +19,7 @@
 // g + 4 of row l % 16 (g = l / 16).  128-bit LDS reads go 16 lanes at a time (0-3, 12-15,
 // 20-27; then 4-11, 16-19, 28-31; the same plus 32): over such 16 lanes the places fall on
 // 16 different 16-byte columns of the 256-byte bank row.
+#include <atomic>
 #include <type_traits>
 
 #include "fp8.h"
@@ -624,9 +626,18 @@ hipError_t launch(const Fp8Product& p, hipStream_t stream) {
   const int64_t by_tiles = (tiles + kXcds - 1) / kXcds * col_blocks, by_cols = (col_blocks + kXcds - 1) / kXcds * tiles;
   const int64_t pairs = kXcds * (by_tiles > by_cols ? by_tiles : by_cols);
   const int64_t most = static_cast<int64_t>(kFp8Cus) * S::per_cu;
-  static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(tile_kernel<S, kOut>), hipFuncAttributeMaxDynamicSharedMemorySize, S::lds);
-  if (attr != hipSuccess) return attr;
+  // the kernel's LDS, allowed once on each device
+  static std::atomic<uint64_t> allowed{0};
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  const uint64_t bit = uint64_t{1} << (dev & 63);
+  if (dev > 63 || !(allowed.load(std::memory_order_relaxed) & bit)) {
+    err = hipFuncSetAttribute(reinterpret_cast<const void*>(tile_kernel<S, kOut>),
+                              hipFuncAttributeMaxDynamicSharedMemorySize, S::lds);
+    if (err != hipSuccess) return err;
+    if (dev < 64) allowed.fetch_or(bit, std::memory_order_relaxed);
+  }
   tile_kernel<S, kOut><<<dim3(static_cast<unsigned>(pairs < most || S::KS > 1 ? pairs : most)), dim3(S::threads), S::lds,
                          stream>>>(p, col_blocks);
   return hipGetLastError();

@@ -501,3 +501,70 @@ def test_gemm_infinite_scale_stays_in_its_row(M, N, K, f32):
     y = gpu_gemm(xq, xs, w, ws, f32)
     assert (y[3] == np.inf).all()
     assert np.isfinite(np.delete(y, 3, 0)).all()
+
+
+@pytest.mark.parametrize("M,N", [(5, 300), (70, 1100), (300, 1100), (300, 2500), (2305, 4100)])
+@pytest.mark.parametrize("f32", [True, False])
+def test_gemm_longest_k(M, N, f32):
+    # K = 65536; the first and last rows against 64-bit products
+    from mxfp4_routed_expert_route_amd import binding
+    K = 65536
+    say("gemm", M, N, K, f32)
+    g = torch.Generator(device="cuda").manual_seed(M + N)
+    byte = lambda *s: torch.randint(0, 256, s, dtype=torch.int32, device="cuda", generator=g)
+    xq, w = byte(M, K), byte(N, K)
+    xq, w = (torch.where((c & 0x7F) == 0x7F, c - 1, c).to(torch.uint8) for c in (xq, w))   # no NaN
+    xs = torch.rand(M, K // 128, device="cuda", generator=g) + 0.5
+    ws = torch.rand(-(-N // 128), K // 128, device="cuda", generator=g) + 0.5
+    y = torch.empty(M, N, dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    binding.moe_gemm_fp8(xq, xs, w, ws, y)
+    torch.cuda.synchronize()
+    rows = sorted({0, 1, M // 2, M - 2, M - 1})
+    table = torch.from_numpy(fp8.decode_e4m3(np.arange(256, dtype=np.uint8))).double().cuda()
+    ref = torch.zeros(len(rows), N, dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(ref)
+    for b in range(0, K // 128, 64):   # 64 runs at a time
+        ks = slice(128 * b, 128 * (b + 64))
+        a = table[xq[rows, ks].long()] * xs[rows, b:b + 64].double().repeat_interleave(128, 1)
+        c = table[w[:, ks].long()] * ws[:, b:b + 64].double().repeat_interleave(128, 1).repeat_interleave(128, 0)[:N]
+        ref += a @ c.t().contiguous()
+        mag += a.abs() @ c.abs().t().contiguous()
+    got = y[rows].double()
+    bound = ((K // 128 + 130) * 2 * U24 + (0.0 if f32 else fp8.MFMA_CUT)) * mag
+    assert ((got - ref).abs() <= bound + (U24 if f32 else BF16_HALF) * (ref.abs() + bound)).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 512, 1024), (70, 1100, 2064), (300, 2500, 400), (2050, 4100, 128)])
+def test_quantize_and_gemm_replayed_beside_other_calls(M, N, K):
+    from mxfp4_routed_expert_route_amd import binding
+    say("graph", M, N, K)
+    rng = np.random.default_rng(M)
+    w, ws = cuda(codes(rng, N, K)), cuda(scales(rng, -(-N // 128), -(-K // 128)))
+    x = cuda(bf16_rows(rng, M, K, 0.5).view(np.int16)).view(torch.bfloat16)
+    other = x.flip(0).contiguous()
+
+    def buffers():
+        return (torch.empty(M, K, dtype=torch.uint8, device="cuda"), torch.empty(M, -(-K // 128), device="cuda"),
+                torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty(M, N, device="cuda"))
+
+    def both(x, b, stream=None):
+        binding.moe_quantize_fp8(x, b[0], b[1], stream=stream)
+        binding.moe_gemm_fp8(b[0], b[1], w, ws, b[2], stream=stream)
+        binding.moe_gemm_fp8(b[0], b[1], w, ws, b[3], stream=stream)
+
+    ref, mine, theirs = buffers(), buffers(), buffers()
+    both(x, ref)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        both(x, mine)
+    for rep in range(3):
+        mine[2].fill_(7), mine[3].fill_(7)
+        torch.cuda.synchronize()
+        g.replay()
+        both(other, theirs, stream=side)      # on another stream meanwhile
+        torch.cuda.synchronize()
+        assert torch.equal(mine[2].view(torch.int16), ref[2].view(torch.int16)), rep
+        assert torch.equal(mine[3].view(torch.int32), ref[3].view(torch.int32)), rep
+        assert torch.equal(theirs[3].flip(0).view(torch.int32), ref[3].view(torch.int32)), rep
