@@ -1,11 +1,10 @@
 // Shared pieces of the block-scaled FP8 (OCP E4M3) kernels.
 #pragma once
-#include "fp8_plan.h"
 #include "config.h"
 #include "device.h"
+#include "fp8_plan.h"
 
 namespace moe {
-
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));

@@ -5,14 +5,15 @@
 // multiplier * partial product in fp32, and the W sums are added in wavefront order through
 // LDS.  A load takes 16 rows x 64 contiguous bytes, the operand's own shape.
 //
-// For outputs of few tiles, which are bound by latency: the LDS-tiled kernel takes about
-// 0.5 us a run of K however little a workgroup has to do, this one runs W of them at a time
-// and meets no barrier before the end.  Measured (us in a graph, N = K = 4096, the tile that
-// the rule below takes / the 64 x 128 LDS tile): 1 row 5.8 / 17.1, 16 rows 7.5 / 17.5, 32
-// rows 10.3 / 20.2, 64 rows 12.4 / 22.5, 128 rows 16.0 / 23.1; a smaller tile than the rule's
+// For outputs of few tiles, which are bound by latency: the LDS-tiled kernel meets a barrier a
+// step, this one none before the end.  Measured (us in a graph, N = K = 4096): 1 row 5.5, 16 rows
+// 7.1 (16 x 16 LDS tiles do not exist; 32 x 32 with K in 4: 7.9).  A smaller tile than the rule's
 // reads the operands more often (16 x 16 tiles, 128 rows: 37.9), a larger one leaves CUs idle
-// (32 x 64 tiles, 16 rows: 14.0).  A single row of N = K = 4096 takes 5.2 us by the kernel
-// trace, of which its 16.8 MB of weights need 2.5.
+// (32 x 64 tiles, 16 rows: 14.0).  All tiles together get about 8 TB/s out of the L2s and the
+// memory behind them (128 rows: 101 MB in 15.6 us less 3), which is why the LDS tiles, whose
+// copies take whole lines, pass it at a long K.  More runs ahead (kDepth 4) change nothing.  A
+// single row of N = K = 4096 takes 5.2 us by the kernel trace: its 16.8 MB of weights need 2.5, a
+// launch's start and end about 2.
 #include "fp8.h"
 #include "fp8_common.h"
 

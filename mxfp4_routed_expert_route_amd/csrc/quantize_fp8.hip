@@ -2,7 +2,9 @@
 //
 // Sixteen lanes take a run, eight elements each: one 16-byte load,
 // the run's maximum by four rotations of the 16-lane row, one 8-byte store; a wavefront
-// does four runs at a time.  Bound by the traffic, 3 bytes an element.
+// does four runs at a time.  Bound by the traffic, 3 bytes an element: 8191 rows of 4096 (101
+// MB) take 18.9 to 22.3 us by the kernel trace, 4.5 to 5.3 TB/s, where a plain copy gets 5.1; 8
+// rows take 2.1 us, a launch's own time.
 #include "fp8.h"
 #include "fp8_common.h"
 
