@@ -3,7 +3,8 @@
     python -m mxfp4_routed_expert_route_amd.build
 
 Compiles every source in csrc/ (object files under _build/) and links the
-shared library.  Also builds the host-only check program of the argument
+shared library.  Also builds the binding's native argument checks (_marshal.so,
+g++ against PyTorch's headers) and the host-only check program of the argument
 validation layer (g++, address and undefined-behaviour sanitizers), which
 the CPU tests run.
 """
@@ -14,12 +15,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_mxfp4.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 VALIDATE_CHECK = os.path.join(BUILD, "validate_check")
 
 ARCH = "gfx950"
@@ -71,6 +74,23 @@ def build_library(verbose: bool = False) -> str:
     return LIB
 
 
+def build_marshal() -> str:
+    """The binding's argument checks, a Python extension module (no GPU code)."""
+    import torch
+    from torch.utils import cpp_extension
+    gxx = shutil.which("g++")
+    if gxx is None:
+        raise RuntimeError("g++ not found")
+    include = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    tmp = MARSHAL + ".tmp"
+    _run([gxx, "-std=c++17", "-O2", "-shared", "-fPIC", "-w", *(f"-I{p}" for p in include),
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          os.path.join(CSRC, "marshal.cc"), "-o", tmp,
+          *(f"-L{p}" for p in cpp_extension.library_paths()), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
+
+
 def build_validate_check() -> str:
     """Host-only build of validate.cpp plus a C driver, with sanitizers (no GPU)."""
     os.makedirs(BUILD, exist_ok=True)
@@ -85,6 +105,7 @@ def build_validate_check() -> str:
 
 def build(verbose: bool = False) -> None:
     build_library(verbose)
+    build_marshal()
     build_validate_check()
 
 
