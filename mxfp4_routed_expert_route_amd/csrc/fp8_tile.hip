@@ -119,7 +119,7 @@ struct Shape {
   static constexpr int lds = h_at + (Nt ? TM * 128 : 0);
   static constexpr int per_cu = 160 * 1024 / lds;        // workgroups of a CU
   static_assert(TM % 16 == 0 && TN % (8 * NW) == 0 && NW % scale_copies == 0 && per_cu >= 1, "shape");
-  static_assert(ST >= 2 && NW % 2 == 0 && (KS == 1 || (NF % 2 == 0 && !Nt)), "copies");
+  static_assert(ST >= 2 && NW % 2 == 0 && NF % 2 == 0 && (KS == 1 || !Nt), "copies");
 };
 
 // Workgroups go through (row tile, column block) pairs; the copies run some steps ahead of the
@@ -662,10 +662,13 @@ hipError_t launch_grouped(int tile_rows, const Fp8Product& p, hipStream_t stream
 // The smallest tile of which the output has at most one per CU (fp8_rows.hip has the smallest).
 // Small tiles are bound by what a step costs beside its products, so K is shared out as well.
 // Measured (us in a graph; the 32 x 64 tile with K in 4 / the rows kernel's / the 64 x 128 tile):
-// 128x4096x4096 11.5 / 15.9 / 18.2, 128x4096x2048 8.2 / 9.7 / 11.2; the 32 x 32 tile with K in 4 /
+// 128x4096x4096 10.7 / 15.9 / 16.7, 128x4096x2048 8.1 / 9.7 / 10.7; the 32 x 32 tile with K in 4 /
 // the rows kernel's: 256x1024x4096 8.6 / 11.8, 64x4096x4096 10.1 / 12.0; the 64 x 64 tile with K
-// in 2 / the 64 x 128 tile: 256x4096x4096 15.5 / 18.2, 256x4096x2048 10.4 / 11.2.  The 64 x 128
+// in 2 / the 64 x 128 tile: 256x4096x4096 13.2 / 16.8, 256x4096x1024 7.2 / 7.6.  The 64 x 128
 // tile gains nothing from K in 2 (512 rows: K = 4096 18.0 / 18.5, 2048 11.7 / 11.4, 1024 8.6 / 7.8).
+// Two wavefronts a SIMD, one reading while the other multiplies, beat one: 64 x 64 15.6 -> 13.2
+// (256x4096x4096), 64 x 128 and a fourth step 18.5 -> 17.5 (512x4096x4096); 128 x 128 as 4 x 2
+// wavefronts instead of 2 x 4 26.9 -> 24.8 (1024x4096x4096).
 // fp32 results, whose products are bf16 MFMAs on converted operands, take the same tiles but the
 // largest (registers); 4096x4096x4096: 130 us with 128 x 256, 172 with 64 x 128.
 template <int kOut>
@@ -674,10 +677,10 @@ hipError_t launch_dense(const Fp8Product& p, hipStream_t stream) {
     return (p.rows + tm - 1) / tm * ((p.n + tn - 1) / tn) <= kFp8Cus;
   };
   if (fits(32, 32)) return launch<Shape<32, 32, 1, 1, 4, false, 4>, kOut>(p, stream);
-  if (fits(32, 64)) return launch<Shape<32, 64, 1, 1, 3, false, 4>, kOut>(p, stream);
-  if (fits(64, 64)) return launch<Shape<64, 64, 1, 2, 3, false, 2>, kOut>(p, stream);
-  if (fits(64, 128)) return launch<Shape<64, 128, 2, 2, 3, false>, kOut>(p, stream);
-  if (fits(128, 128)) return launch<Shape<128, 128, 2, 4, 4, false>, kOut>(p, stream);
+  if (fits(32, 64)) return launch<Shape<32, 64, 1, 2, 3, false, 4>, kOut>(p, stream);
+  if (fits(64, 64)) return launch<Shape<64, 64, 2, 2, 4, false, 2>, kOut>(p, stream);
+  if (fits(64, 128)) return launch<Shape<64, 128, 2, 4, 4, false>, kOut>(p, stream);
+  if (fits(128, 128)) return launch<Shape<128, 128, 4, 2, 4, false>, kOut>(p, stream);
   if (kOut == kFp8OutF32 || fits(128, 256)) return launch<Shape<128, 256, 2, 4, 3, false>, kOut>(p, stream);
   if constexpr (kOut == kFp8OutBf16) return launch<Shape<256, 256, 2, 4, 2, false>, kOut>(p, stream);
 }
