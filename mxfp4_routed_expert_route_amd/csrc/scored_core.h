@@ -13,8 +13,9 @@
 // pass computes them in fp32 and looks at every comparison that the answer rests on (each
 // chosen key against the next one; with groups, the last group taken against the first
 // left).  If one of them is closer than the two fp32 keys can be off, the token is done
-// again with fp64 keys.  With E = 256 normal logits and a bias of sigma 0.1 that is about
-// one token in a hundred.  Without a bias the scores' order is the logits', which are
+// again with fp64 keys.  With E = 256, k = 6, normal logits and a bias of sigma 0.1 that
+// is one token in 40,000 (softmax) or 1,600 (sigmoid); such a token's wavefront then takes
+// about 2 us longer.  Without a bias the scores' order is the logits', which are
 // compared as they are; only sums of two scores (group_top 2) are then rounded.
 //   Error of an fp32 key, u = 2^-24: sigmoid = 1 / (1 + e^-l): e^-l within 3u, the sum u, the
 //   reciprocal 2u: at most 6u of a score <= 1.  Softmax: the argument l - m is rounded
