@@ -141,3 +141,15 @@ def test_binding_refuses_cpu_tensors_shapes_and_types(lib):
                  lambda: binding.moe_grouped_ffn_fp8(x, 1, x, None, None, None, None, None, None, 0.0, None, None)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_native_argument_checks_are_in_use(lib):
+    assert binding._arg is binding._marshal.arg
+    x = torch.zeros(2, 4)
+    for bad, match in (((x, (torch.float32,), (2, 4), -1, "x"), "GPU tensor"),
+                       ((x, (torch.int32,), (2, 4), 0, "x"), "must be torch.int32"),
+                       ((None, (torch.float32,), (2, 4), 0, "x"), "got None")):
+        with pytest.raises(ValueError, match=match):
+            binding._arg(*bad)
+    with pytest.raises(TypeError):
+        binding._arg(x)
