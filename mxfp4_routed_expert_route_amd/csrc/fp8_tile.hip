@@ -149,7 +149,9 @@ void tile_kernel(Fp8Product p, int col_blocks) {
 
   // Consecutive workgroups go to the XCDs in turn: XCD x takes row tiles x, x + 8, ..., all
   // column blocks of one from one L2; its workgroups share out the pairs in turn.  With few row
-  // tiles it takes column blocks x, x + 8, ... instead where that spreads the pairs more evenly.
+  // tiles it takes column blocks x, x + 8, ... instead where that spreads the pairs more evenly
+  // (the FFN of two tokens 70 -> 63 us) or, as evenly, reads fewer bytes: by rows all 8 L2s read all
+  // the weights, by columns all the activations (512x4096x2048 13.5 -> 11.2 us).
   const int xcd = blockIdx.x % kXcds;
   const int stride = gridDim.x / kXcds;
   const int most_t = (n_tiles + kXcds - 1) / kXcds * col_blocks;   // the pairs of one XCD
@@ -378,7 +380,8 @@ void tile_kernel(Fp8Product p, int col_blocks) {
           for (int m = 0; m < (NS > 0 ? NS : 1); ++m) {
             const bool last = m + 1 >= NS;
             // Where the copies go: streaming shapes, at once behind the barrier; the 256 x 256 tile,
-            // some ahead of each of the first half's fragments; the others, behind the first
+            // some ahead of each of the first half's fragments (its copies are one step ahead only:
+            // behind the MFMAs, 8191 x 4096 x 4096 takes 136 instead of 127 us); the others, behind the first
             // fragment's MFMAs (a CU takes in one such copy every 16 cycles, and the wavefronts
             // stand meanwhile), unless the step has no other fragment before its wait.
             constexpr bool kAfter = kLate && NS >= 2 && MT * NF <= 16;
