@@ -96,7 +96,8 @@ moe_status moe_grouped_ffn_fp8(const uint16_t* x, int64_t T, int32_t H, int32_t 
                                uint16_t* y_sorted, void* ws, size_t ws_bytes, void* stream);
 
 /* Workspace bytes of moe_grouped_ffn_fp8, also enough for moe_expert_offsets and the
- * routing calls at these sizes.  0 for invalid sizes. */
+ * routing calls at these sizes.  It does not shrink as T grows, so a workspace for the largest
+ * batch serves the smaller ones.  0 for invalid sizes. */
 size_t moe_fp8_workspace_bytes(int64_t T, int32_t E, int32_t k, int32_t H, int32_t I);
 
 #ifdef __cplusplus

@@ -57,7 +57,9 @@ moe_status fp8_workspace_layout(int64_t T, int32_t E, int32_t k, int32_t H, int3
   L.xs = take(t * (H / 128) * sizeof(float));
   L.hq = take(slots * I);
   L.hs = take(slots * (I / 128) * sizeof(float));
-  L.plan = take(256 + static_cast<size_t>(L.tile_bound) * sizeof(RowTile));
+  // room for the smallest tiles, whatever the rule takes: the size then never shrinks as T grows
+  L.plan = take(256 + static_cast<size_t>(ffn_tile_bound(static_cast<int64_t>(slots), E, kFfnMinTileRows)) *
+                          sizeof(RowTile));
   L.total = end > routing.offsets_bytes ? end : routing.offsets_bytes;
   *out = L;
   return MOE_OK;

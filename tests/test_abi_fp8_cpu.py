@@ -153,3 +153,9 @@ def test_native_argument_checks_are_in_use(lib):
             binding._arg(*bad)
     with pytest.raises(TypeError):
         binding._arg(x)
+
+
+@pytest.mark.parametrize("E,k,H,I", [(256, 6, 128, 128), (8, 2, 128, 128), (1, 1, 128, 256), (64, 8, 256, 512), (1024, 8, 128, 128)])
+def test_ffn_workspace_never_shrinks_with_the_batch(lib, E, k, H, I):
+    sizes = [binding.moe_fp8_workspace_bytes(T, E, k, H, I) for T in range(1, 6000)]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:])) and sizes[0] > 0
