@@ -11,19 +11,23 @@
 //
 // Order.  The keys are ordered as 64-bit arithmetic orders them, at fp32's price: a first
 // pass computes them in fp32 and looks at every comparison that the answer rests on (each
-// chosen key against the next one; with groups, the last group taken against the first
-// left).  If one of them is closer than the two fp32 keys can be off, the token is done
-// again with fp64 keys.  With E = 256, k = 6, normal logits and a bias of sigma 0.1 that
-// is one token in 40,000 (softmax) or 1,600 (sigmoid); such a token's wavefront then takes
-// about 2 us longer.  Without a bias the scores' order is the logits', which are
-// compared as they are; only sums of two scores (group_top 2) are then rounded.
+// chosen key against the next one; with groups, those taken against those left).  If one of
+// them is closer than the fp32 keys can be off, the token is done again with fp64 keys.  With
+// E = 256, k = 6, normal logits and a bias of sigma 0.1 that is one token in 40,000 (softmax)
+// or 1,600 (sigmoid); such a token's wavefront then takes about 2 us longer.  Without a bias
+// the scores' order is the logits', which are compared as they are; only sums of two scores
+// (group_top 2) are then rounded.
 //   Error of an fp32 key, u = 2^-24: sigmoid = 1 / (1 + e^-l): e^-l within 3u, the sum u, the
 //   reciprocal 2u: at most 6u of a score <= 1.  Softmax: the argument l - m is rounded
 //   (u |l - m|), the exponential adds 3u; the sum, taken in fp64, is off by at most
 //   sum_e p_e (u d_e + 3u) <= u (3 + ln E) (d_e = m - l_e, and sum p d <= ln E); its reciprocal
 //   and the product 3u; so p is off by at most p u (d + 3) + 10 p u + 3 p u <= 16.4 u pmax, as
 //   p d <= 0.37 pmax.  Adding the bias rounds by u |key|.  Two keys: 35 u max(smax, |key|)
-//   in all; kKeyTol is 40 u, for sums of two keys twice that.
+//   in all; kKeyTol is 40 u.  A group's key is one or two of these: off by at most 33 u smax and
+//   u times the sum of its terms' magnitudes, and as much again for rounding their sum, which
+//   may be far smaller than they are (biases of opposite sign).  With a kGroupTol of 36 u for
+//   smax and a kTermTol of 4 u for the magnitudes there is room for rounding the bound itself.
+//   Each group has its own error, so all that are taken are compared with all that are left.
 //
 // Selection.  Up to 8 keys a lane are sorted there first (largest first, equal ones by slot),
 // and each of the k rounds then takes the wave-wide maximum of the lanes' first keys and moves
@@ -42,7 +46,7 @@ struct ScoreArgs {
   int lane_bits;     // log2 L
 };
 
-constexpr float kKeyTol = 40 * 0x1p-24f;
+constexpr float kKeyTol = 40 * 0x1p-24f, kGroupTol = 36 * 0x1p-24f, kTermTol = 4 * 0x1p-24f;
 
 // Order-preserving bits; 0: no expert here or already taken, 1: excluded expert.
 __device__ __forceinline__ uint32_t key_bits(float f) { return order_bits(f); }
@@ -256,15 +260,19 @@ __device__ __forceinline__ bool select_experts(const float (&l)[EPL], const floa
       k2 = lo > s ? lo : s;
     }
     Key gk = k1;
-    const bool summed = a.group_top == 2;
-    if (summed && k1 > 1) {
-      F v;
+    const bool summed = a.group_top == 2, rounded = has_bias || summed;   // else logits, as they are
+    const bool counted = k1 > 1;
+    F v = 0, size = 0;   // the group's key, and its terms' magnitudes
+    if (rounded && counted) {
+      const bool two = summed && k2 > 1;
       if (has_bias) {
-        v = key_value(k1);
-        if (k2 > 1) v += key_value(k2);
+        const F v1 = key_value(k1), v2 = two ? key_value(k2) : F(0);
+        v = v1 + v2;
+        size = fabs(v1) + fabs(v2);
       } else {
         v = score(key_value(static_cast<uint32_t>(k1)));
-        if (k2 > 1) v += score(key_value(static_cast<uint32_t>(k2)));
+        if (two) v += score(key_value(static_cast<uint32_t>(k2)));
+        size = v;
       }
       gk = key_bits(v);
     }
@@ -274,12 +282,14 @@ __device__ __forceinline__ bool select_experts(const float (&l)[EPL], const floa
       rank += (ok > gk || (ok == gk && o < g)) ? 1 : 0;
     }
     const bool live = g < a.groups, kept = live && rank < a.topk_groups;
-    if (kCheck && (has_bias || summed) && a.topk_groups < a.groups) {
-      // the last group taken against the first left (excluded groups give NaN: decided)
-      const F last = key_value(static_cast<Key>(~wave_max(static_cast<Key>(kept ? ~gk : 0))));
-      const F next = key_value(wave_max(static_cast<Key>(live && !kept ? gk : 0)));
-      const F unit = fmax(static_cast<F>(smax), fmax(fabs(last), fabs(next)));
-      if (last - next <= F(2) * F(kKeyTol) * unit) return false;
+    if (kCheck && rounded && a.topk_groups < a.groups) {
+      // every group taken, at its least, against every group left, at its most (groups of excluded
+      // experts only are left last in any arithmetic: not counted)
+      const F err = F(kGroupTol) * static_cast<F>(smax) + F(kTermTol) * size;
+      const Key least = static_cast<Key>(~wave_max(static_cast<Key>(kept && counted ? ~key_bits(v - err) : 0)));
+      const Key most = wave_max(static_cast<Key>(live && !kept && counted ? key_bits(v + err) : 0));
+      if (most != 0 && least <= most) return false;
+      if (__builtin_amdgcn_ballot_w64(counted && !(err < __builtin_inff()))) return false;   // past fp32's range
     }
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
