@@ -212,7 +212,9 @@ moe_status moe_route_and_group(const float* logits, int64_t T, int32_t E, int32_
  *          groups = 1: every expert can.
  *   topk_ids[t][0..k-1]   the k largest keys, key descending
  *   topk_weights[t][j]    scale * s_(chosen j), with renormalize != 0 divided by
- *                         the sum of the k chosen scores (0 if that sum is 0)
+ *                         the sum of the k chosen scores (0 if that sum is 0).
+ *                         Small scores keep 64 bits until the quotient: sigmoid
+ *                         scores are 0 for logits below -709.78 only
  * Equal keys, of experts or of groups, go to the lower index.  Keys are ordered
  * as in 64-bit arithmetic: keys that fp32 cannot tell apart are compared again
  * in fp64.  Without a bias, experts are ordered by their logits, whose order

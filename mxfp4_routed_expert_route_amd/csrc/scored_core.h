@@ -413,15 +413,13 @@ __device__ __forceinline__ void route_scored_token(const Logit* __restrict__ row
   if (a.renormalize) {
     div = 0.0;
     for (int j = 0; j < k; ++j) div += read_lane(s, j);
-    // sums that fp32 does not hold well: both sides up by 2^200
-    if (div < 0x1p-100) {
-      s *= 0x1p+200;
-      div *= 0x1p+200;
-    }
   } else if (a.score == 0) {
     div = st.sum;
   }
-  const float q = static_cast<float>(s) / static_cast<float>(div);
+  // scores of a small sum may be denormal in fp32, or 0: divided in fp64 (sigmoid only: the
+  // other sums are 1 or more).  From 2^-20 on what fp32 loses of a score is below 2^-130 of the sum.
+  const float q = div < 0x1p-20 ? static_cast<float>(s / div)   // uniform
+                                : static_cast<float>(s) / static_cast<float>(div);
   my_weight = div > 0.0 ? a.scale * q : 0.f;
 }
 

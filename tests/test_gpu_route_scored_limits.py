@@ -1,5 +1,5 @@
 """Scored routing where fp32 arithmetic runs out, on the GPU against the float64 oracle: group
-keys whose two terms cancel.  Ids equal, weights within 2^-20
+keys whose two terms cancel, and scores below fp32's range.  Ids equal, weights within 2^-20
 relative (fp32 exponential and quotient: 14 u at most, u = 2^-24, and one rounding)."""
 from __future__ import annotations
 
@@ -92,3 +92,20 @@ def test_group_sums_past_the_range_of_fp32():
         check(logits, 2, bias, score="sigmoid", groups=3, topk_groups=keep, group_top=2)
     check(logits, 2, -bias, score="sigmoid", groups=3, topk_groups=2, group_top=2)
 
+
+# ------------------------------------------------------------ scores below the range of fp32
+
+@pytest.mark.parametrize("groups,keep,top", [(1, 1, 1), (4, 2, 1), (4, 2, 2), (8, 8, 2)])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_sigmoid_scores_below_fp32(groups, keep, top, renormalize):
+    rng = np.random.default_rng(groups)
+    at = np.array([-59, -61, -70, -86, -88, -100, -103, -120, -170, -226, -230, -241, -242, -250, -300, -500, -700], np.float32)
+    logits = (at[:, None] + rng.permutation(16)[None] * 0.5).astype(np.float32)
+    # a large score among small ones: quotients of scores that fp32 holds as denormals or not at all
+    wide = rng.uniform(-200, -40, (60, 16)).astype(np.float32)
+    bias = (rng.standard_normal(16) * 0.1).astype(np.float32)
+    for l in (logits, wide):
+        for k in (1, 4):
+            check(l, k, score="sigmoid", groups=groups, topk_groups=keep, group_top=top, renormalize=renormalize)
+    check(logits[5:], 4, bias, score="sigmoid", groups=groups, topk_groups=keep, group_top=top,
+          renormalize=renormalize, scale=2.5)
