@@ -46,20 +46,21 @@ __device__ __forceinline__ i32x4 lds_rsrc(const void* base, uint32_t bytes) {
 // range check takes voff alone: rows that are not there have to show in voff, and lanes past the
 // resource get zeros.  In assembly so that the compiler, which cannot tell the steps' LDS apart,
 // does not wait for all copies before every LDS read; wait_copies counts them.  They write no
-// register.
+// register: the LDS address is an operand in m0, which the compiler sets (the nop is the cycle
+// between that and its use).
 template <bool kNt>   // kNt: non-temporal
 __device__ __forceinline__ void copy16(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
   if constexpr (kNt)
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
-                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen nt lds"
+                 :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
   else
-    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
-                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
+    asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
 }
 // 4 bytes a lane from rsrc + voff + soff to LDS address lds + 4 * lane.
 __device__ __forceinline__ void copy4(i32x4 rsrc, uint32_t voff, uint32_t soff, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
-               :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
+  asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
+               :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
 }
 template <int kLeft>
 __device__ __forceinline__ void wait_copies() {
