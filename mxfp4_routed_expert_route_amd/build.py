@@ -92,14 +92,17 @@ def build_marshal() -> str:
 
 
 def build_validate_check() -> str:
-    """Host-only build of validate.cpp plus a C driver, with sanitizers (no GPU)."""
+    """Host-only build of validate.cpp, validate_fp8.cpp and a C driver, with sanitizers (no GPU)."""
     os.makedirs(BUILD, exist_ok=True)
     gxx = shutil.which("g++")
     if gxx is None:
         raise RuntimeError("g++ not found")
+    tmp = f"{VALIDATE_CHECK}.{os.getpid()}"   # two test processes may build it at once
     _run([gxx, "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined",
           "-fno-omit-frame-pointer", os.path.join(CSRC, "validate.cpp"),
-          os.path.join(CSRC, "host_check", "validate_check.cpp"), "-o", VALIDATE_CHECK])
+          os.path.join(CSRC, "validate_fp8.cpp"),
+          os.path.join(CSRC, "host_check", "validate_check.cpp"), "-o", tmp])
+    os.replace(tmp, VALIDATE_CHECK)
     return VALIDATE_CHECK
 
 

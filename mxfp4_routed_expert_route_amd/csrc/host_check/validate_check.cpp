@@ -1,11 +1,14 @@
 // Host-only driver for the argument checks (built with g++ and sanitizers, no GPU).
 // Forces every status code of every entry point's check from the host and checks
 // the workspace layout; exits non-zero on the first mismatch.
+#include <climits>
 #include <cstdio>
 #include <cstdlib>
 
 #include "../config.h"
+#include "../fp8_plan.h"
 #include "../validate.h"
+#include "../validate_fp8.h"
 
 using namespace moe;
 
@@ -118,6 +121,70 @@ int main() {
   expect("comb y misaligned", check_combine(p, p, p, 16, 256, 6, p4), MOE_ERR_MISALIGNED);
   expect("comb null", check_combine(p, nullptr, p, 16, 256, 6, p), MOE_ERR_INVALID_ARGUMENT);
   expect("comb T=0", check_combine(nullptr, nullptr, nullptr, 0, 256, 6, nullptr), MOE_OK);
+
+  // scored routing
+  auto scored = [&](int64_t T, int32_t E, int32_t k, int32_t groups, int32_t topk, int32_t top) {
+    return check_route_scored(p, MOE_F32, T, E, k, MOE_SCORE_SIGMOID, p, groups, topk, top, p, p);
+  };
+  expect("scored ok", scored(16, 256, 6, 8, 4, 2), MOE_OK);
+  expect("scored largest T", scored(INT32_MAX / 8, 1024, 8, 64, 64, 1), MOE_OK);
+  expect("scored T*k overflow", scored(INT32_MAX / 8 + 1, 1024, 8, 64, 64, 1), MOE_ERR_UNSUPPORTED);
+  expect("scored largest int64 T", scored(INT64_MAX, 256, 6, 8, 4, 2), MOE_ERR_UNSUPPORTED);
+  expect("scored least int64 T", scored(INT64_MIN, 256, 6, 8, 4, 2), MOE_ERR_INVALID_ARGUMENT);
+  expect("scored largest groups", scored(16, 256, 6, INT32_MAX, INT32_MAX, 2), MOE_ERR_INVALID_ARGUMENT);
+  expect("scored least groups", scored(16, 256, 6, INT32_MIN, INT32_MIN, 2), MOE_ERR_INVALID_ARGUMENT);
+  expect("scored largest topk_groups", scored(16, 256, 6, 8, INT32_MAX, 2), MOE_ERR_INVALID_ARGUMENT);
+  expect("scored largest E and k", scored(16, INT32_MAX, INT32_MAX, 1, 1, 2), MOE_ERR_UNSUPPORTED);
+  expect("scored misaligned", check_route_scored(odd, MOE_BF16, 16, 256, 6, MOE_SCORE_SOFTMAX, p, 1, 1, 1, p, p), MOE_ERR_MISALIGNED);
+
+  // quantisation
+  expect("quantise ok", check_quantize_fp8(p, INT32_MAX, kMaxDim, p, p), MOE_OK);
+  expect("quantise rows", check_quantize_fp8(p, INT64_MAX, kMaxDim, p, p), MOE_ERR_UNSUPPORTED);
+  expect("quantise K", check_quantize_fp8(p, 1, INT32_MAX, p, p), MOE_ERR_UNSUPPORTED);
+  expect("quantise least K", check_quantize_fp8(p, 1, INT32_MIN, p, p), MOE_ERR_INVALID_ARGUMENT);
+  expect("quantise misaligned", check_quantize_fp8(p, 1, 256, p4, p), MOE_ERR_MISALIGNED);
+
+  // dense product
+  auto dense = [&](int64_t M, int32_t N, int32_t K) {
+    return check_gemm_fp8(p, p, M, N, K, p, p, MOE_BF16, p, nullptr, 0);
+  };
+  expect("dense ok", dense(16, 256, 128), MOE_OK);
+  expect("dense largest M", dense(INT32_MAX, 128, kMaxDim), MOE_OK);
+  expect("dense M * N", dense(INT32_MAX, 129, kMaxDim), MOE_ERR_UNSUPPORTED);
+  expect("dense largest N", dense(1 << 14, kFp8MaxN, kMaxDim), MOE_OK);
+  expect("dense N", dense(1, kFp8MaxN + 1, 128), MOE_ERR_UNSUPPORTED);
+  expect("dense largest int64 M", dense(INT64_MAX, INT32_MAX, 128), MOE_ERR_UNSUPPORTED);
+  expect("dense misaligned", check_gemm_fp8(p, p, 16, 256, 128, p, p, MOE_F32, p4, nullptr, 0), MOE_ERR_MISALIGNED);
+
+  // grouped FP8 FFN: the largest activations and experts, and one step past them
+  auto ffn8 = [&](int64_t T, int32_t E, int32_t k, int32_t H, int32_t I, size_t ws_bytes) {
+    return check_ffn_fp8(p, T, H, I, E, k, p, p, p, p, p, p, p, p, p, ws_bytes);
+  };
+  struct { int64_t T; int32_t E, k, H, I; } sizes[] = {
+      {1, 1, 1, 128, 128}, {8, 256, 6, 4096, 2048}, {8191, 256, 6, 4096, 2048}, {kMaxActivationBytes / 256, 1024, 1, 128, 128},
+      {kMaxActivationBytes / 2 / 8 / 65536, 8, 8, 65536, 128}, {16, 2, 1, 65536, 32752 / 128 * 128}, {16, 2, 1, 128, 65536}};
+  for (const auto& z : sizes) {
+    Fp8WsLayout L8;
+    expect("fp8 layout", fp8_workspace_layout(z.T, z.E, z.k, z.H, z.I, &L8), MOE_OK);
+    const int64_t slots = z.T * z.k;
+    const size_t ends[] = {L8.xs, L8.hq, L8.hs, L8.plan, L8.total};
+    const size_t need[] = {L8.xq + static_cast<size_t>(z.T) * z.H, L8.xs + static_cast<size_t>(z.T) * (z.H / 128) * 4,
+                           L8.hq + static_cast<size_t>(slots) * z.I, L8.hs + static_cast<size_t>(slots) * (z.I / 128) * 4,
+                           L8.plan + 256 + static_cast<size_t>(L8.tile_bound) * sizeof(RowTile)};
+    for (int i = 0; i < 5; ++i)
+      if (ends[i] < need[i]) { std::printf("FAIL fp8 layout part %d, T = %lld\n", i, static_cast<long long>(z.T)); ++failures; }
+    if (L8.tile_bound < 1 || L8.tile_bound > INT32_MAX) { std::printf("FAIL fp8 tile bound\n"); ++failures; }
+    expect("fp8 ffn ok", ffn8(z.T, z.E, z.k, z.H, z.I, L8.total), MOE_OK);
+    expect("fp8 ffn small ws", ffn8(z.T, z.E, z.k, z.H, z.I, L8.total - 1), MOE_ERR_WORKSPACE_TOO_SMALL);
+  }
+  expect("fp8 ffn activations", ffn8(kMaxActivationBytes / 256 + 1, 1024, 1, 128, 128, SIZE_MAX), MOE_ERR_UNSUPPORTED);
+  expect("fp8 ffn expert", ffn8(1, 2, 1, 65536, 32768, SIZE_MAX), MOE_ERR_UNSUPPORTED);
+  expect("fp8 ffn largest H and I", ffn8(1, 2, 1, 65536, 65536, SIZE_MAX), MOE_ERR_UNSUPPORTED);
+  expect("fp8 ffn int32 H and I", ffn8(1, 2, 1, INT32_MAX / 128 * 128, INT32_MAX / 128 * 128, SIZE_MAX), MOE_ERR_UNSUPPORTED);
+  expect("fp8 ffn largest int64 T", ffn8(INT64_MAX, 1024, 8, 65536, 128, SIZE_MAX), MOE_ERR_UNSUPPORTED);
+  expect("fp8 ffn T * k", ffn8(INT32_MAX, 1024, 1, 65536, 128, SIZE_MAX), MOE_ERR_UNSUPPORTED);
+  expect("fp8 ffn misaligned", check_ffn_fp8(p4, 16, 128, 128, 4, 2, p, p, p, p, p, p, p, p, p, 1 << 20), MOE_ERR_MISALIGNED);
+  if (failures == 0) std::printf("scored routing and fp8 checks ok\n");
 
   if (failures) return 1;
   std::printf("validate_check ok\n");

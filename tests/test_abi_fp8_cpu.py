@@ -159,3 +159,10 @@ def test_native_argument_checks_are_in_use(lib):
 def test_ffn_workspace_never_shrinks_with_the_batch(lib, E, k, H, I):
     sizes = [binding.moe_fp8_workspace_bytes(T, E, k, H, I) for T in range(1, 6000)]
     assert all(a <= b for a, b in zip(sizes, sizes[1:])) and sizes[0] > 0
+
+
+def test_host_checks_run_under_sanitizers():
+    # the checks and the workspace layout at the ends of their ranges, with address and undefined-behaviour checks
+    r = subprocess.run([build_mod.build_validate_check()], capture_output=True, text=True)
+    assert r.returncode == 0 and not r.stderr, r.stdout + r.stderr
+    assert "scored routing and fp8 checks ok" in r.stdout
