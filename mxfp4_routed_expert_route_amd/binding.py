@@ -275,6 +275,7 @@ def moe_read_probe(buf, sink, stream=None):
 E4M3 = (torch.float8_e4m3fn, torch.uint8)
 SCORES = {"softmax": 0, "sigmoid": 1}
 LOGIT_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+_LOGITS = tuple(LOGIT_TYPES)
 FP8_BLOCK = 128
 
 
@@ -305,7 +306,8 @@ try:   # the same checks natively (csrc/marshal.cc), 0.1 us a tensor instead of 
 except ImportError:   # not built, or for another PyTorch
     pass
 else:
-    _marshal.set_refuse(_arg)
+    _refuse = _arg
+    _marshal.set_refuse(_refuse)
     _arg = _marshal.arg
 
 
@@ -348,7 +350,7 @@ def _scored(logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups,
     if kind is None:
         raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
     dev = logits.get_device()
-    return (_arg(logits, LOGIT_TYPES, (T, E), dev, "logits"), kind, T, E, k, SCORES[score],
+    return (_arg(logits, _LOGITS, (T, E), dev, "logits"), kind, T, E, k, SCORES[score],
             None if bias is None else _arg(bias, _F32, (E,), dev, "bias"),
             groups, topk_groups, group_top, 1 if renormalize else 0, scale,
             _arg(topk_ids, _I32, (T, k), dev, "topk_ids"),

@@ -568,3 +568,25 @@ def test_quantize_and_gemm_replayed_beside_other_calls(M, N, K):
         assert torch.equal(mine[2].view(torch.int16), ref[2].view(torch.int16)), rep
         assert torch.equal(mine[3].view(torch.int32), ref[3].view(torch.int32)), rep
         assert torch.equal(theirs[3].flip(0).view(torch.int32), ref[3].view(torch.int32)), rep
+
+
+def test_right_arguments_pass_the_native_checks():
+    """A right call never reaches the Python function that words the refusals."""
+    from mxfp4_routed_expert_route_amd import _marshal, binding, layer
+    T, E, k, H, I = 20, 8, 2, 256, 128
+    t = to_gpu(ffn_inputs(np.random.default_rng(3), T, E, k, H, I))
+    b = layer.LayerBuffers.allocate_fp8(T, E, k, H, I)
+    q, s = torch.empty(T, H, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(T, 2, device="cuda")
+    refused = []
+    _marshal.set_refuse(lambda *a: refused.append(a[4]))
+    try:
+        for dtype in (torch.float32, torch.bfloat16):
+            dev = dict(logits=torch.zeros(T, E, dtype=dtype, device="cuda"), x=t["x"], w1=t["w1"], w1_s=t["w1s"],
+                       w2=t["w2"], w2_s=t["w2s"])
+            layer.run_layer_fp8(dev, b, 10.0, bias=torch.zeros(E, device="cuda"))
+        binding.moe_quantize_fp8(t["x"], q, s)
+        binding.moe_gemm_fp8(q, s, t["w1"][0], t["w1s"][0], torch.empty(T, 2 * I, device="cuda"))
+    finally:
+        _marshal.set_refuse(binding._refuse)
+    torch.cuda.synchronize()
+    assert not refused
