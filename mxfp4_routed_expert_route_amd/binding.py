@@ -339,6 +339,20 @@ def _runs(n: int) -> int:
     return -(-n // FP8_BLOCK)
 
 
+_END32 = 2 ** 31   # ctypes cuts a number to the C type's bits without a word
+
+
+def _refuse_past_32_bits(**numbers):
+    for name, v in numbers.items():
+        if not -_END32 <= v < _END32:
+            raise ValueError(f"{name} = {v} does not fit 32 bits")
+
+
+def _sizes(rows: int, *sizes: int) -> bool:
+    """Whether a row count and sizes arrive as they are (64 and 32 bits)."""
+    return rows < 2 ** 63 and all(v < _END32 for v in sizes) and min(rows, *sizes) >= 0
+
+
 def _scored(logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups, group_top,
             renormalize, scale):
     if logits.dim() != 2:
@@ -349,6 +363,9 @@ def _scored(logits, k, topk_ids, topk_weights, score, bias, groups, topk_groups,
     kind = LOGIT_TYPES.get(logits.dtype)
     if kind is None:
         raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if not (E < _END32 and -_END32 <= k < _END32 and -_END32 <= groups < _END32
+            and -_END32 <= topk_groups < _END32 and -_END32 <= group_top < _END32):
+        _refuse_past_32_bits(E=E, k=k, groups=groups, topk_groups=topk_groups, group_top=group_top)
     dev = logits.get_device()
     return (_arg(logits, _LOGITS, (T, E), dev, "logits"), kind, T, E, k, SCORES[score],
             None if bias is None else _arg(bias, _F32, (E,), dev, "bias"),
@@ -388,6 +405,8 @@ def moe_quantize_fp8(x, q, scale, stream=None):
     if x.dim() != 2:
         raise ValueError("x must be [rows, K]")
     rows, K = x.shape
+    if K >= _END32:
+        _refuse_past_32_bits(K=K)
     dev = x.get_device()
     _run("moe_quantize_fp8", dev, stream, _arg(x, BF16, (rows, K), dev, "x"), rows, K,
          _arg(q, E4M3, (rows, K), dev, "q"),
@@ -395,6 +414,8 @@ def moe_quantize_fp8(x, q, scale, stream=None):
 
 
 def moe_gemm_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
+    if not _sizes(M, N, K):
+        return 0
     return int(load().moe_gemm_fp8_workspace_bytes(M, N, K))
 
 
@@ -405,6 +426,8 @@ def moe_gemm_fp8(xq, x_scale, w, w_scale, y, ws=None, stream=None):
         raise ValueError("xq must be [M, K] and w [N, K]")
     M, K = xq.shape
     N = w.shape[0]
+    if K >= _END32 or N >= _END32:
+        _refuse_past_32_bits(K=K, N=N)
     dev, nk = xq.get_device(), _runs(K)
     kind = 0 if y.dtype is torch.float32 else 1
     _run("moe_gemm_fp8", dev, stream, _arg(xq, E4M3, (M, K), dev, "xq"),
@@ -414,6 +437,8 @@ def moe_gemm_fp8(xq, x_scale, w, w_scale, y, ws=None, stream=None):
 
 
 def moe_fp8_workspace_bytes(T: int, E: int, k: int, H: int, I: int) -> int:
+    if not _sizes(T, E, k, H, I):
+        return 0
     return int(load().moe_fp8_workspace_bytes(T, E, k, H, I))
 
 
@@ -425,6 +450,8 @@ def moe_grouped_ffn_fp8(x, k: int, w1, w1_scale, w2, w2_scale, counts, offsets, 
         raise ValueError("x must be [T, H] and w1 [E, 2I, H]")
     T, H = x.shape
     E, I = w1.shape[0], w1.shape[1] // 2
+    if not (H < _END32 and I < _END32 and E < _END32 and -_END32 <= k < _END32):
+        _refuse_past_32_bits(H=H, I=I, E=E, k=k)
     dev = x.get_device()
     _run("moe_grouped_ffn_fp8", dev, stream, _arg(x, BF16, (T, H), dev, "x"), T, H, I, E, k,
          _arg(w1, E4M3, (E, 2 * I, H), dev, "w1"),

@@ -40,3 +40,45 @@ def test_every_argument_is_given_to_the_native_checks_as_they_take_it(monkeypatc
     for call in _calls():
         call()
     assert seen.count("logits") == 4 and len(seen) == 2 * 4 + 2 * 9 + 3 + 6 + 5 + 10
+
+
+@pytest.mark.parametrize("name", ["groups", "topk_groups", "group_top"])
+@pytest.mark.parametrize("value", [2 ** 32 + 1, -2 ** 32 + 1, 2 ** 31, -2 ** 31 - 1])
+def test_numbers_past_32_bits_are_refused(name, value):
+    # the C interface takes 32-bit sizes, and ctypes cuts a larger one down without a word
+    logits = torch.zeros(2, 8)
+    out = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2)
+    with pytest.raises(ValueError, match=name):
+        binding.moe_route_scored(logits, 2, *out, **{name: value})
+
+
+def test_shapes_past_32_bits_are_refused():
+    # shapes alone (no memory); 2^32 + 128 would arrive as 128
+    big = 2 ** 32 + 128
+    meta = lambda *s, dtype=torch.uint8: torch.empty(s, dtype=dtype, device="meta")
+    f32 = lambda *s: meta(*s, dtype=torch.float32)
+    i32 = lambda *s: meta(*s, dtype=torch.int32)
+    bf16 = lambda *s: meta(*s, dtype=torch.bfloat16)
+    for call, match in (
+            (lambda: binding.moe_route_scored(f32(1, big), 2, i32(1, 2), f32(1, 2)), "E = "),
+            (lambda: binding.moe_route_scored(f32(1, 8), big, i32(1, big), f32(1, big)), "k = "),
+            (lambda: binding.moe_route_scored_and_group(f32(1, big), 2, i32(1, 2), f32(1, 2), i32(1, big // 32), i32(big),
+                                                        i32(big + 1), i32(2), i32(2), meta(64)), "E = "),
+            (lambda: binding.moe_quantize_fp8(bf16(1, big), meta(1, big), f32(1, big // 128)), "K = "),
+            (lambda: binding.moe_gemm_fp8(meta(1, big), f32(1, big // 128), meta(1, big), f32(1, big // 128), f32(1, 1)), "K = "),
+            (lambda: binding.moe_gemm_fp8(meta(1, 128), f32(1, 1), meta(big, 128), f32(big // 128, 1), f32(1, big)), "N = "),
+            (lambda: binding.moe_grouped_ffn_fp8(bf16(1, big), 1, meta(1, 256, big), f32(1, 2, big // 128), meta(1, big, 128),
+                                                 f32(1, big // 128, 1), i32(1), i32(2), i32(1), 0.0, bf16(1, big), meta(64)), "H = "),
+            (lambda: binding.moe_grouped_ffn_fp8(bf16(1, 128), 1, meta(1, 2 * big, 128), f32(1, big // 64, 1), meta(1, 128, big),
+                                                 f32(1, 1, big // 128), i32(1), i32(2), i32(1), 0.0, bf16(1, 128), meta(64)), "I = "),
+            (lambda: binding.moe_grouped_ffn_fp8(bf16(1, 128), 1, meta(big, 256, 128), f32(big, 2, 1), meta(big, 128, 128),
+                                                 f32(big, 1, 1), i32(big), i32(big + 1), i32(1), 0.0, bf16(1, 128), meta(64)), "E = "),
+            (lambda: binding.moe_grouped_ffn_fp8(bf16(1, 128), big, meta(4, 256, 128), f32(4, 2, 1), meta(4, 128, 128),
+                                                 f32(4, 1, 1), i32(4), i32(5), i32(big), 0.0, bf16(big, 128), meta(64)), "k = ")):
+        with pytest.raises(ValueError, match=match):
+            call()
+    # sizes are checked by the calls that ask for a workspace too: none for what no call takes
+    assert binding.moe_fp8_workspace_bytes(16, big, 6, 4096, 2048) == 0
+    assert binding.moe_fp8_workspace_bytes(16, 256, 6, big, 2048) == 0
+    assert binding.moe_fp8_workspace_bytes(2 ** 64 + 16, 256, 6, 4096, 2048) == 0
+    assert binding.moe_gemm_fp8_workspace_bytes(4, big, 128) == 0
