@@ -178,9 +178,10 @@ def moe_grouped_ffn_mxfp4(x, k: int, w1, w1_scale, w2, w2_scale, counts, offsets
 def moe_combine(y_sorted, topk_weights, scatter, y, stream=None):
     T, k = topk_weights.shape
     H = y.shape[1]
-    _check("moe_combine", load().moe_combine(
-        _ptr(y_sorted, BF16, "y_sorted"), _ptr(topk_weights, torch.float32, "topk_weights"),
-        _ptr(scatter, torch.int32, "scatter"), T, H, k, _ptr(y, BF16, "y"), _stream(stream)))
+    # on y's GPU, like the scored-routing and FP8 calls whose rows it sums
+    _run("moe_combine", y.get_device(), stream,
+         _ptr(y_sorted, BF16, "y_sorted"), _ptr(topk_weights, torch.float32, "topk_weights"),
+         _ptr(scatter, torch.int32, "scatter"), T, H, k, _ptr(y, BF16, "y"))
 
 
 def moe_forward_mxfp4(logits, x, k: int, w1, w1_scale, w2, w2_scale, swiglu_limit: float,

@@ -82,3 +82,74 @@ def test_shapes_past_32_bits_are_refused():
     assert binding.moe_fp8_workspace_bytes(16, 256, 6, big, 2048) == 0
     assert binding.moe_fp8_workspace_bytes(2 ** 64 + 16, 256, 6, 4096, 2048) == 0
     assert binding.moe_gemm_fp8_workspace_bytes(4, big, 128) == 0
+
+
+def test_the_fp8_layer_runs_on_its_tensors_gpu(monkeypatch):
+    # tensors on GPU 1 while GPU 0 is current: every call of the layer goes to GPU 1's stream
+    import contextlib
+    import dataclasses
+
+    from mxfp4_routed_expert_route_amd import layer
+
+    T, E, k, H, I = 4, 8, 2, 128, 128
+
+    class OnGpu1:
+        """A tensor's face, as the binding looks at it."""
+        is_cuda = True
+
+        def __init__(self, dtype, *shape):
+            self.dtype, self.shape = dtype, torch.Size(shape)
+
+        def dim(self):
+            return len(self.shape)
+
+        def numel(self):
+            return self.shape.numel()
+
+        def get_device(self):
+            return 1
+
+        device = property(lambda self: torch.device("cuda", 1))
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 4096
+
+    i32, f32, bf16, u8 = (lambda *s, d=d: OnGpu1(d, *s) for d in (torch.int32, torch.float32, torch.bfloat16, torch.uint8))
+    b = layer.LayerBuffers(T, E, k, H, I, i32(T, k), f32(T, k), i32(T, 1), i32(E), i32(E + 1), i32(T * k), i32(T * k),
+                           bf16(T * k, H), bf16(T, H), u8(1 << 16))
+    assert len(dataclasses.fields(b)) == 15
+    dev = dict(logits=f32(T, E), x=bf16(T, H), w1=u8(E, 2 * I, H), w1_s=f32(E, 2, 1), w2=u8(E, H, I), w2_s=f32(E, 1, 1))
+    current, calls = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], d
+        yield
+        current[0] = before
+
+    class Stream:
+        def __init__(self, dev):
+            self.cuda_stream = 1000 + dev
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: calls.append((name, current[0], a[-1])) or 0
+
+    monkeypatch.setattr(binding, "_arg", lambda t, *a: t.data_ptr())
+    monkeypatch.setattr(binding, "load", Lib)
+    monkeypatch.setattr(binding, "_fns", {})
+    monkeypatch.setattr(binding, "_several", None)
+    monkeypatch.setattr(binding, "_raw_stream", lambda dev: 1000 + dev)
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev=None: Stream(current[0] if dev is None else dev))
+    monkeypatch.setattr(torch.cuda, "device", device)
+    layer.run_layer_fp8(dev, b, 10.0)
+    assert calls == [(n, 1, 1001) for n in ("moe_route_scored_and_group", "moe_grouped_ffn_fp8", "moe_combine")]
+    calls.clear()
+    layer.run_layer_fp8(dev, b, 10.0, stream=77)
+    assert calls == [(n, 1, 77) for n in ("moe_route_scored_and_group", "moe_grouped_ffn_fp8", "moe_combine")]
+    assert current == [0]
