@@ -52,8 +52,8 @@ moe_status moe_quantize_fp8(const uint16_t* x, int64_t rows, int32_t K, uint8_t*
  *   w        e4m3 [N][K]                         16-byte aligned
  *   w_scale  fp32 [ceil(N/128)][ceil(K/128)]
  *   y        bf16 or fp32 [M][N], by y_type      out; 16-byte aligned
- *   ws       workspace of at least moe_gemm_fp8_workspace_bytes(M, N, K) bytes,
- *            16-byte aligned; contents on entry are ignored (NULL where that is 0)
+ *   ws       workspace of moe_gemm_fp8_workspace_bytes(M, N, K) bytes, 16-byte aligned.  That
+ *            is 0 at every size: no tile of the product uses any, and NULL with 0 bytes will do
  * K is a positive multiple of 16, at most 65536; N >= 1, at most 2^24; M * N at most
  * 2^38.  M = 0 enqueues nothing.
  */
@@ -61,7 +61,7 @@ moe_status moe_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, int3
                         const uint8_t* w, const float* w_scale, int32_t y_type, void* y, void* ws,
                         size_t ws_bytes, void* stream);
 
-/* Workspace bytes of moe_gemm_fp8 (0 for invalid sizes or where none is used). */
+/* Workspace bytes of moe_gemm_fp8: 0. */
 size_t moe_gemm_fp8_workspace_bytes(int64_t M, int32_t N, int32_t K);
 
 /*

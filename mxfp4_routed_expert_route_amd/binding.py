@@ -415,14 +415,15 @@ def moe_quantize_fp8(x, q, scale, stream=None):
 
 
 def moe_gemm_fp8_workspace_bytes(M: int, N: int, K: int) -> int:
+    """0 at every size."""
     if not _sizes(M, N, K):
         return 0
     return int(load().moe_gemm_fp8_workspace_bytes(M, N, K))
 
 
 def moe_gemm_fp8(xq, x_scale, w, w_scale, y, ws=None, stream=None):
-    """y [M, N] (bf16 or fp32) = X W^T of block-scaled E4M3 xq [M, K] and w [N, K]; ws holds
-    moe_gemm_fp8_workspace_bytes(M, N, K) bytes (None where that is 0)."""
+    """y [M, N] (bf16 or fp32) = X W^T of block-scaled E4M3 xq [M, K] and w [N, K].  No size
+    needs a workspace (moe_gemm_fp8_workspace_bytes is 0)."""
     if xq.dim() != 2 or w.dim() != 2:
         raise ValueError("xq must be [M, K] and w [N, K]")
     M, K = xq.shape

@@ -6,7 +6,7 @@
 namespace moe {
 
 hipError_t launch_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, int N, int K,
-                           const uint8_t* w, const float* w_scale, bool f32, void* y, void*,
+                           const uint8_t* w, const float* w_scale, bool f32, void* y,
                            hipStream_t stream) {
   Fp8Product p{};
   p.act = xq;

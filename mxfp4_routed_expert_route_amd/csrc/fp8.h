@@ -50,7 +50,7 @@ hipError_t launch_fp8_dense(const Fp8Product& p, hipStream_t stream);
 hipError_t launch_fp8_grouped(int tile_rows, const Fp8Product& p, hipStream_t stream);
 
 hipError_t launch_gemm_fp8(const uint8_t* xq, const float* x_scale, int64_t M, int N, int K,
-                           const uint8_t* w, const float* w_scale, bool f32, void* y, void* ws,
+                           const uint8_t* w, const float* w_scale, bool f32, void* y,
                            hipStream_t stream);
 
 struct Fp8WsLayout;

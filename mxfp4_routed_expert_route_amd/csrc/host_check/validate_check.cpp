@@ -146,7 +146,7 @@ int main() {
 
   // dense product
   auto dense = [&](int64_t M, int32_t N, int32_t K) {
-    return check_gemm_fp8(p, p, M, N, K, p, p, MOE_BF16, p, nullptr, 0);
+    return check_gemm_fp8(p, p, M, N, K, p, p, MOE_BF16, p, nullptr);
   };
   expect("dense ok", dense(16, 256, 128), MOE_OK);
   expect("dense largest M", dense(INT32_MAX, 128, kMaxDim), MOE_OK);
@@ -154,7 +154,7 @@ int main() {
   expect("dense largest N", dense(1 << 14, kFp8MaxN, kMaxDim), MOE_OK);
   expect("dense N", dense(1, kFp8MaxN + 1, 128), MOE_ERR_UNSUPPORTED);
   expect("dense largest int64 M", dense(INT64_MAX, INT32_MAX, 128), MOE_ERR_UNSUPPORTED);
-  expect("dense misaligned", check_gemm_fp8(p, p, 16, 256, 128, p, p, MOE_F32, p4, nullptr, 0), MOE_ERR_MISALIGNED);
+  expect("dense misaligned", check_gemm_fp8(p, p, 16, 256, 128, p, p, MOE_F32, p4, nullptr), MOE_ERR_MISALIGNED);
 
   // grouped FP8 FFN: the largest activations and experts, and one step past them
   auto ffn8 = [&](int64_t T, int32_t E, int32_t k, int32_t H, int32_t I, size_t ws_bytes) {

@@ -65,8 +65,6 @@ moe_status fp8_workspace_layout(int64_t T, int32_t E, int32_t k, int32_t H, int3
   return MOE_OK;
 }
 
-size_t gemm_fp8_workspace(int64_t, int32_t, int32_t) { return 0; }
-
 moe_status check_route_scored(const void* logits, int32_t logits_type, int64_t T, int32_t E,
                               int32_t k, int32_t score, const void* bias, int32_t groups,
                               int32_t topk_groups, int32_t group_top, const void* ids,
@@ -100,19 +98,17 @@ moe_status check_quantize_fp8(const void* x, int64_t rows, int32_t K, const void
 
 moe_status check_gemm_fp8(const void* xq, const void* xs, int64_t M, int32_t N, int32_t K,
                           const void* w, const void* ws, int32_t y_type, const void* y,
-                          const void* work, size_t work_bytes) {
+                          const void* work) {
   if (M < 0 || N < 1 || K < 1) return MOE_ERR_INVALID_ARGUMENT;
   if (y_type != MOE_F32 && y_type != MOE_BF16) return MOE_ERR_INVALID_ARGUMENT;
   if (K % 16 != 0 || K > kMaxDim || N > kFp8MaxN || M > INT32_MAX ||
       M * static_cast<int64_t>(N) > kFp8MaxOut)
     return MOE_ERR_UNSUPPORTED;
   if (M == 0) return MOE_OK;
-  const size_t need = gemm_fp8_workspace(M, N, K);
-  if (!xq || !xs || !w || !ws || !y || (need > 0 && !work)) return MOE_ERR_INVALID_ARGUMENT;
+  if (!xq || !xs || !w || !ws || !y) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(xq, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(xs, 4) ||
       !aligned(ws, 4) || !aligned(work, 16))
     return MOE_ERR_MISALIGNED;
-  if (work_bytes < need) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return MOE_OK;
 }
 

@@ -17,7 +17,6 @@ struct Fp8WsLayout {
 
 moe_status fp8_workspace_layout(int64_t T, int32_t E, int32_t k, int32_t H, int32_t I,
                                 Fp8WsLayout* out);
-size_t gemm_fp8_workspace(int64_t M, int32_t N, int32_t K);
 
 moe_status check_route_scored(const void* logits, int32_t logits_type, int64_t T, int32_t E,
                               int32_t k, int32_t score, const void* bias, int32_t groups,
@@ -27,7 +26,7 @@ moe_status check_quantize_fp8(const void* x, int64_t rows, int32_t K, const void
                               const void* scale);
 moe_status check_gemm_fp8(const void* xq, const void* xs, int64_t M, int32_t N, int32_t K,
                           const void* w, const void* ws, int32_t y_type, const void* y,
-                          const void* work, size_t work_bytes);
+                          const void* work);
 moe_status check_ffn_fp8(const void* x, int64_t T, int32_t H, int32_t I, int32_t E, int32_t k,
                          const void* w1, const void* w1s, const void* w2, const void* w2s,
                          const void* counts, const void* offsets, const void* gather,

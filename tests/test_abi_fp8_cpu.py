@@ -166,3 +166,12 @@ def test_host_checks_run_under_sanitizers():
     r = subprocess.run([build_mod.build_validate_check()], capture_output=True, text=True)
     assert r.returncode == 0 and not r.stderr, r.stdout + r.stderr
     assert "scored routing and fp8 checks ok" in r.stdout
+
+
+def test_gemm_takes_no_workspace(lib):
+    # 0 bytes at every size, and a call without a workspace is refused for its misaligned y alone
+    for M, N, K in ((1, 1, 16), (1, 256, 4096), (64, 256, 16384), (512, 4096, 2048), (8191, 4096, 4096), (17, 70000, 144)):
+        assert lib.moe_gemm_fp8_workspace_bytes(M, N, K) == 0
+        for kind in (0, 1):
+            assert lib.moe_gemm_fp8(P, P, M, N, K, P, P, kind, P + 8, None, 0, None) == MISALIGNED
+            assert lib.moe_gemm_fp8(P, P, M, N, K, P, P, kind, P + 8, P, 0, None) == MISALIGNED
