@@ -11,7 +11,10 @@
  *   activations  e4m3 [rows][K], scales fp32 [rows][ceil(K/128)]: one per run
  *   weights      e4m3 [N][K], scales fp32 [ceil(N/128)][ceil(K/128)]: one per
  *                block of 128 rows and one run
- * A value is element * scale.  Scales may be any finite fp32.
+ * A value is element * scale.  Scales may be any finite fp32 whose products are finite: a
+ * product of matrices multiplies each run's sum by x_scale * w_scale, rounded to fp32 first, so
+ * one that overflows gives an infinity (NaN beside a sum of 0), and one below 2^-126 keeps its
+ * bits down to 2^-149 only.  Scales that moe_quantize_fp8 makes are between 2^-109 and 2^120.
  */
 #ifndef MOE_FP8_H
 #define MOE_FP8_H

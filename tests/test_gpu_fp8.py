@@ -590,3 +590,23 @@ def test_right_arguments_pass_the_native_checks():
         _marshal.set_refuse(binding._refuse)
     torch.cuda.synchronize()
     assert not refused
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 260, 656), (20, 260, 656), (70, 1100, 2064), (300, 300, 656), (300, 2500, 400),
+                                   (2305, 4097, 272)])
+@pytest.mark.parametrize("f32", [True, False])
+def test_gemm_scales_at_the_ends_of_their_range(M, N, K, f32):
+    # products of scales up to 2^127, on a run of zero codes and on one of the smallest codes, and
+    # down to 2^-126
+    say("gemm scales", M, N, K, f32)
+    rng = np.random.default_rng(M + N)
+    xq, w = codes(rng, M, K), codes(rng, N, K)
+    nk = -(-K // 128)
+    xs, ws = scales(rng, M, nk), scales(rng, -(-N // 128), nk)
+    xs[:, 1], ws[:, 1] = 2.0 ** 63, -2.0 ** 64
+    xs[::3, 2], ws[:, 2] = 2.0 ** -100, 2.0 ** -26
+    xq[:, 128:256] = 0
+    gemm_close(gpu_gemm(xq, xs, w, ws, f32), xq, xs, w, ws, f32)
+    xq[::2, 128:256] = 1
+    w[:, 128:256] = 1
+    gemm_close(gpu_gemm(xq, xs, w, ws, f32), xq, xs, w, ws, f32)
