@@ -73,10 +73,11 @@ size_t moe_gemm_fp8_workspace_bytes(int64_t M, int32_t N, int32_t K);
  *
  * For expert e and each row p in [offsets[e], offsets[e+1]), token t = gather[p] / k:
  *   x[t] is quantised as by moe_quantize_fp8;
- *   g = x[t] . W1[e][i],  u = x[t] . W1[e][I+i]           (moe_gemm_fp8's product, as for bf16)
+ *   g = x[t] . W1[e][i],  u = x[t] . W1[e][I+i]           (moe_gemm_fp8's product: as for fp32
+ *                          up to 90 rows per expert on average, above that as for bf16)
  *   h[i] = SiLU(min(g, limit)) * clamp(u, -limit, limit)  (fp32)
  *   h is quantised from fp32 by moe_quantize_fp8's rule;
- *   y_sorted[p][n] = h . W2[e][n], rounded once to bf16.
+ *   y_sorted[p][n] = h . W2[e][n] (as for bf16), rounded once to bf16.
  * A limit <= 0 or not finite disables the clamp.
  *
  *   x         bf16  [T][H]                   16-byte aligned

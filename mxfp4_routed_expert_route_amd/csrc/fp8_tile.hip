@@ -129,7 +129,10 @@ struct Shape {
 template <class S, int kOut>
 __global__ __launch_bounds__(S::threads, S::NW / 4 * S::per_cu)
 void tile_kernel(Fp8Product p, int col_blocks) {
-  constexpr bool kSwiglu = kOut == kFp8OutSwiglu, kFull = kOut == kFp8OutF32;
+  constexpr bool kSwiglu = kOut == kFp8OutSwiglu;
+  // which products (mfma_e4m3): the streaming shapes wait for weights, so the gates and ups of
+  // h get fp32's there
+  constexpr bool kFull = kOut == kFp8OutF32 || (kSwiglu && S::Nt);
   constexpr int MT = S::MT, NF = S::NF, NR = 16 * NF;
   // Steps the copies are ahead.  Streaming shapes fill a step's LDS as soon as its barrier says it
   // has been read; the others a little later, spread over the next step's fragments.

@@ -610,3 +610,29 @@ def test_gemm_scales_at_the_ends_of_their_range(M, N, K, f32):
     xq[::2, 128:256] = 1
     w[:, 128:256] = 1
     gemm_close(gpu_gemm(xq, xs, w, ws, f32), xq, xs, w, ws, f32)
+
+
+@pytest.mark.parametrize("shape", [(8, 8, 4, 1024, 512), (1, 8, 8, 2048, 1024), (64, 64, 4, 512, 512), (100, 4, 2, 1024, 512)], ids=str)
+def test_ffn_of_few_rows_an_expert_keeps_fp32_gates(shape):
+    """16-, 32- and 96-row tiles, normal data, against the exact result rounded to bf16.
+
+    A gate off by d of its size moves a share d / s of h's codes by one step, s <= 2^-3 of the
+    code, so y by sqrt(d s) of its 2-norm.  fp32 products and sums, exponential and reciprocal:
+    about 16 u, 3.5e-4.  W2's product moves some of y's roundings, 2.5e-4 (a cut of 1.4e-5 against
+    a step of 2^-7, as above).  2^-10 is twice both together; gates off by 1.4e-5, which the FP8
+    matrix instruction would make, are at 1.3e-3.
+    """
+    say("ffn gates", shape)
+    T, E, k, H, I = shape
+    rng = np.random.default_rng(T)
+    d = ffn_inputs(rng, *shape)
+    d["x"] = bf16_rows(rng, T, H, 0.0)
+    for n, K in (("w1", H), ("w2", I)):
+        d[n] = fp8.round_e4m3(np.clip(rng.standard_normal(d[n].shape) * 90, -448, 448))
+        d[n + "s"] = scales(rng, *d[n + "s"].shape, size=1 / (90 * K ** 0.5))
+    ref, _ = fp8.ffn_fp8(inputs.bf16_bits_to_f32(d["x"]), d["gather"], d["offsets"], k, d["w1"], d["w1s"], d["w2"],
+                         d["w2s"], 10.0)
+    ref = torch.from_numpy(ref).to(torch.bfloat16).double().numpy()
+    off = np.linalg.norm(gpu_ffn(d, 10.0) - ref) / np.linalg.norm(ref)
+    say("off by", off)
+    assert off <= 2.0 ** -10
