@@ -76,7 +76,8 @@ size_t moe_gemm_fp8_workspace_bytes(int64_t M, int32_t N, int32_t K);
  *   g = x[t] . W1[e][i],  u = x[t] . W1[e][I+i]           (moe_gemm_fp8's product: as for fp32
  *                          up to 90 rows per expert on average, above that as for bf16)
  *   h[i] = SiLU(min(g, limit)) * clamp(u, -limit, limit)  (fp32)
- *   h is quantised from fp32 by moe_quantize_fp8's rule;
+ *   h is quantised from fp32 by moe_quantize_fp8's rule, the quotient 448 h / a being within
+ *   2^-22 of itself before it is rounded to E4M3;
  *   y_sorted[p][n] = h . W2[e][n] (as for bf16), rounded once to bf16.
  * A limit <= 0 or not finite disables the clamp.
  *

@@ -17,7 +17,10 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 // remainder fma(-q0, m, t) give the correctly rounded quotient; a quotient of an 11-bit
 // by an 8-bit number that is not on a border of E4M3 is further from it than fp32's
 // rounding, so rounding it again to E4M3 is one rounding of the true quotient.
-// Five operations an element, where an IEEE division takes about ten.
+// Five operations an element, where an IEEE division takes about ten.  For fp32 x (the FFN's
+// h) t is rounded as well: the quotient is off by at most 2^-23 and its own rounding, under
+// 2^-22, so a code is the neighbour of the nearest one where 448 x / a is that close to the
+// border between them.
 struct RunScale {
   float scale, c, m, r;
 };
