@@ -180,3 +180,29 @@ def test_more_tokens_than_one_launch_takes():
     assert torch.equal(b.counts.long(), torch.bincount(want.flatten().long(), minlength=E))
     p = 1 / (1 + np.exp(-1.0))
     assert (b.topk_weights.double() - torch.tensor([p, 1 - p], dtype=torch.float64, device="cuda")).abs().max() < 1e-6
+
+
+@pytest.mark.parametrize("T,E,k,groups", [(1, 256, 6, 8), (16, 64, 4, 1), (64, 32, 6, 4), (200, 16, 3, 4), (600, 16, 2, 1)])
+def test_scored_routing_in_front_of_the_mxfp4_experts(T, E, k, groups):
+    """Scored routing in moe_route's place: the MXFP4 FFN and the combine take its outputs."""
+    from mxfp4_routed_expert_route_amd import binding, layer
+    from tests.test_gpu_parity import ffn_close, tiny
+    H, I = 256, 128
+    print(f"[route_scored] mxfp4 T={T} E={E} k={k} groups={groups}", file=sys.stderr, flush=True)
+    inp = tiny(T, E, k, H, I, 70 + T)
+    dev = layer.to_device(inp)
+    b = layer.LayerBuffers.allocate(T, E, k, H, I)
+    b.ws.fill_(0x5A)
+    bias = (np.random.default_rng(T).standard_normal(E) * 0.1).astype(np.float32)
+    how = dict(score="sigmoid", groups=groups, topk_groups=(groups + 1) // 2, scale=2.5)
+    binding.moe_route_scored_and_group(dev["logits"], k, b.topk_ids, b.topk_weights, b.bitmatrix, b.counts, b.offsets,
+                                       b.gather, b.scatter, b.ws, bias=torch.from_numpy(bias).cuda(), **how)
+    layer.run_ffn(dev, b, 10.0)
+    torch.cuda.synchronize()
+    ids, w = fp8.route_scored(inp["logits"], k, bias=bias, **how)
+    assert np.array_equal(b.topk_ids.cpu().numpy(), ids)
+    counts, offsets, gather, scatter = oracle.expert_offsets(ids, E)
+    assert np.array_equal(b.gather.cpu().numpy(), gather) and np.array_equal(b.scatter.cpu().numpy(), scatter)
+    ys = oracle.ffn(inp["x"], gather, offsets, k, inp["w1"], inp["w1_s"], inp["w2"], inp["w2_s"], 10.0)
+    ffn_close(layer.bf16_tensor_to_f32(b.y_sorted), ys)
+    ffn_close(layer.bf16_tensor_to_f32(b.y), oracle.combine(ys, w.astype(np.float32), scatter, T, k))
