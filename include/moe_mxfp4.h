@@ -245,7 +245,7 @@ moe_status moe_route_scored(const void* logits, int32_t logits_type, int64_t T, 
 /*
  * moe_route_scored_and_group -- moe_route_scored, moe_build_bitmatrix and
  * moe_expert_offsets in one call, with exactly their outputs (one launch for
- * T <= 64, as moe_route_and_group).  ws is the workspace of moe_expert_offsets.
+ * a few tokens).  ws is the workspace of moe_expert_offsets.
  * T = 0 writes zeros to counts and offsets.
  */
 moe_status moe_route_scored_and_group(const void* logits, int32_t logits_type, int64_t T,

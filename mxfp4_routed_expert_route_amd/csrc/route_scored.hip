@@ -1,8 +1,7 @@
 // Scored routing (softmax or sigmoid scores, balance bias, expert groups): one wavefront
-// per token (route_scored_token in scored_core.h).  As for plain top-k, up to 64 tokens
-// are routed and grouped by expert in one launch of one workgroup (at most 8 experts per
-// lane); above, the routing kernel also writes the bit matrix and the expert-offsets
-// kernels follow.
+// per token (route_scored_token in scored_core.h).  As for plain top-k, a few tokens are
+// routed and grouped by expert in one launch of one workgroup (one_launch has the rule);
+// above, the routing kernel also writes the bit matrix and the expert-offsets kernels follow.
 //
 // Bound by the vector ALU: about 610 instructions a token (E = 256, softmax and bias), of which
 // the k + 1 rounds are a quarter.  8191 tokens take 12.2 us by the kernel trace (10.6 in a row of
@@ -72,9 +71,14 @@ ScoreArgs score_args(const ScoredRouting& r, int E) {
 
 // At most 32: per / L < 2 E / 64.
 int experts_per_lane(const ScoreArgs& a) { return (a.per + (1 << a.lane_bits) - 1) >> a.lane_bits; }
-// One launch up to this many experts per lane: with 16 wavefronts a workgroup has 128
-// registers a lane, and 16 or 32 experts per lane would spill there.
-constexpr int kFrontMaxPerLane = 8;
+// One launch for a few tokens: its 16 wavefronts take them in turn, while the routing and
+// offsets kernels spread them over the GPU.  Measured (us in a graph, softmax and bias, k = 6),
+// one launch / those kernels: 256 experts 8 tokens 6.6 / 11.3, 16 8.4 / 11.2, 24 10.0 / 11.2, 25
+// 11.5 / 11.3, 64 23 / 11.5; 64 experts 24 7.7 / 8.6, 32 9.3 / 8.6.  With 8 experts a lane the
+// one-launch form spills (128 registers a lane with 16 wavefronts; 164 bytes of scratch): 512
+// experts 1 token 14.9 / 20.2, 8 19.9 / 21.6, 12 25.0 / 21.5, 64 94 / 22.
+bool one_launch(int64_t T, int epl) { return epl <= 4 ? T <= 24 : epl <= 8 && T <= 8; }
+static_assert(kFrontMaxTokens >= 24, "the workgroup's LDS");
 
 template <class Logit>
 hipError_t launch_route(const Logit* logits, int64_t T, int E, int k, const ScoreArgs& a,
@@ -144,7 +148,7 @@ hipError_t launch_route_scored_and_group(const void* logits, bool bf16, int64_t 
                                          int32_t* gather, int32_t* scatter, void* ws,
                                          hipStream_t stream) {
   const ScoreArgs a = score_args(r, E);
-  if (T > kFrontMaxTokens || experts_per_lane(a) > kFrontMaxPerLane) {
+  if (!one_launch(T, experts_per_lane(a))) {
     const hipError_t err = launch_route_scored(logits, bf16, T, E, k, r, ids, weights, bm, stream);
     if (err != hipSuccess) return err;
     return launch_offsets(bm, ids, T, E, k, counts, offsets, gather, scatter, ws, stream);

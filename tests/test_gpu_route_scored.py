@@ -206,3 +206,9 @@ def test_scored_routing_in_front_of_the_mxfp4_experts(T, E, k, groups):
     ys = oracle.ffn(inp["x"], gather, offsets, k, inp["w1"], inp["w1_s"], inp["w2"], inp["w2_s"], 10.0)
     ffn_close(layer.bf16_tensor_to_f32(b.y_sorted), ys)
     ffn_close(layer.bf16_tensor_to_f32(b.y), oracle.combine(ys, w.astype(np.float32), scatter, T, k))
+
+
+@pytest.mark.parametrize("T,E,groups", [(24, 256, 8), (25, 256, 1), (24, 40, 1), (25, 40, 5), (8, 512, 1), (9, 512, 1),
+                                        (8, 300, 3), (9, 300, 3), (24, 512, 64), (24, 65, 13)])
+def test_and_group_on_both_sides_of_the_one_launch_rule(T, E, groups):
+    test_and_group_equals_the_separate_calls(T, E, 6 if E // groups > 5 else 2, groups)
