@@ -73,9 +73,9 @@ __device__ __forceinline__ uint32_t row16_max_u32(uint32_t v) {
 // kFull true (fp32 results, which would show it, and h in smaller tiles): four bf16 MFMAs on
 // operands converted exactly; products and sums keep fp32's 24 bits, at about half the rate.
 //
-// h shows the cut too: a gate off by 1.4e-5 moves one code of h in some thousands by a step, and the FFN's
-// error against 64 bits is 0.0018 to 0.0021 of y's 2-norm, with full products 0.00166, which is
-// bf16's rounding.  They cost 256 experts (H = 4096, I = 2048, k = 6) 174 -> 176 us for 8 tokens
+// h shows the cut too: a gate off by 1.4e-5 moves one code of h in some thousands by a step, and
+// the FFN's error against 64 bits is 0.0018 to 0.0021 of y's 2-norm, with full products 0.00166,
+// which is bf16's rounding.  They cost 256 experts (H = 4096, I = 2048, k = 6) 174 -> 176 us for 8 tokens
 // (16-row tiles), 1028 -> 1030 for 512 (32) and 1190 -> 1219 for 2048 (96), but 1490 -> 2550 for
 // 8191 skewed ones (256).  W2's product, whose result is only rounded, gains nothing by them.
 __device__ __forceinline__ bf16x8 e4m3_to_bf16(int lo, int hi) {
