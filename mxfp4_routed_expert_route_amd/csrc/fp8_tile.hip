@@ -678,6 +678,9 @@ hipError_t launch_grouped(int tile_rows, const Fp8Product& p, hipStream_t stream
 // wavefronts instead of 2 x 4 26.9 -> 24.8 (1024x4096x4096).
 // fp32 results, whose products are bf16 MFMAs on converted operands, take the same tiles but the
 // largest (registers); 4096x4096x4096: 130 us with 128 x 256, 172 with 64 x 128.
+// Up to 32 rows of more than 65536 columns are a stream of weights, as the grouped FFN's are, and
+// take its tile; the 256 x 256 tile (fp32: 128 x 256) / it: 1x70000x4096 114 / 55 (fp32 104 / 55),
+// 32x70000x4096 120 / 62, 32x131072x1024 38.5 / 25.7, 1x131072x4096 140 / 87 (6.2 TB/s).
 template <int kOut>
 hipError_t launch_dense(const Fp8Product& p, hipStream_t stream) {
   auto fits = [&](int tm, int tn) {
@@ -688,7 +691,9 @@ hipError_t launch_dense(const Fp8Product& p, hipStream_t stream) {
   if (fits(64, 64)) return launch<Shape<64, 64, 2, 2, 4, false, 2>, kOut>(p, stream);
   if (fits(64, 128)) return launch<Shape<64, 128, 2, 4, 4, false>, kOut>(p, stream);
   if (fits(128, 128)) return launch<Shape<128, 128, 4, 2, 4, false>, kOut>(p, stream);
-  if (kOut == kFp8OutF32 || fits(128, 256)) return launch<Shape<128, 256, 2, 4, 3, false>, kOut>(p, stream);
+  if (fits(128, 256)) return launch<Shape<128, 256, 2, 4, 3, false>, kOut>(p, stream);
+  if (p.rows <= 32) return launch<Shape<32, 256, 1, 4, 2, true>, kOut>(p, stream);
+  if constexpr (kOut == kFp8OutF32) return launch<Shape<128, 256, 2, 4, 3, false>, kOut>(p, stream);
   if constexpr (kOut == kFp8OutBf16) return launch<Shape<256, 256, 2, 4, 2, false>, kOut>(p, stream);
 }
 

@@ -636,3 +636,12 @@ def test_ffn_of_few_rows_an_expert_keeps_fp32_gates(shape):
     off = np.linalg.norm(gpu_ffn(d, 10.0) - ref) / np.linalg.norm(ref)
     say("off by", off)
     assert off <= 2.0 ** -10
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 66001, 656), (5, 65600, 1040), (32, 66000, 272), (33, 66000, 272)])
+@pytest.mark.parametrize("f32", [True, False])
+def test_gemm_few_rows_of_very_many_columns(M, N, K, f32):
+    test_gemm_every_tile(M, N, K, f32)
+    if M > 3:
+        test_gemm_beside_other_tensors(M, N, K, f32)
+        test_gemm_infinite_scale_stays_in_its_row(M, N, K, f32)
