@@ -18,14 +18,15 @@ constexpr int kFp8Cus = 256;   // CUs of an MI355X: how far tiles are cut to giv
 // bound by the weights, an expert's rows are to fit one tile (each weight is then read once) and
 // all CUs are to have a workgroup; from 90 rows on it is bound by the products and takes 256.
 // Measured (us; H = 4096, I = 2048, k = 6 unless said; random routing):
-//   96 / 256 rows: 256 experts 84 rows on average 1325 / 1637, 96 1680 / 1662, 128 2341 / 1729;
-//     64 experts 80 364 / 445, 96 448 / 453, 128 602 / 469.
-//   32 / 96 rows: 256 experts 20 1042 / 1059, 24 1101 / 1068; 64 experts 20 266 / 292, 24 316 / 296.
-//   16 / 32 rows: 256 experts 2 845 / 854, 6 1009 / 970, 12 1143 / 991; 64 experts 3 270 / 251, 12
-//     314 / 259.  Few tokens leave no second workgroup for a CU, and 16-row tiles keep more copies
-//     on their way: 256 experts, 1 token 50 / 68, 2 70 / 76, 6 164 / 179, 8 186 / 190, 12 255 / 252.
-//   Fewer first-product workgroups than CUs (8 experts, k = 2), 16 / 32 / 96: 4 rows 57 / 71, 12 61
-//     / 72, 16 - / 72 / 60; at 256 workgroups (16 experts) 12 rows 115 / 88 / 88.
+//   96 / 256 rows: 256 experts 84 rows on average 1522 / 1706, 96 2004 / 1694, 128 2659 / 1745;
+//     64 experts 80 423 / 441, 90 437 / 462, 96 509 / 453, 128 678 / 474.
+//   32 / 96 rows: 256 experts 20 1070 / 1065, 24 1116 / 1075; 64 experts 20 277 / 296, 24 319 / 306.
+//   16 / 32 rows: 256 experts 2 849 / 888, 6 1046 / 1012, 12 1143 / 1032; 64 experts 3 272 / 255, 12
+//     325 / 270.  Few tokens leave no second workgroup for a CU, and 16-row tiles keep more copies
+//     on their way: 256 experts, 1 token 57 / 66, 2 63 / 77, 6 172 / 187, 8 186 / 201, 12 259 / 262.
+//   Fewer first-product workgroups than CUs (k = 2), 16 / 32 / 96: 8 experts 2 rows 53 / 67 / 55, 12
+//     56 / 69 / 59, 20 57 / 69 / 60; 16 experts of I = 1024 8 50 / 60 / 51, 12 56 / 60 / 54, 20 56 /
+//     61 / 55; at 256 workgroups (16 experts) 12 rows 117 / 92 / 92.
 inline int fp8_tile_rows(int64_t T, int E, int k, int I) {
   const int64_t slots = T * k, avg_rows = slots / E;
   if (avg_rows > 90) return 256;

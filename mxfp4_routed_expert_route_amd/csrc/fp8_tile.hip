@@ -23,8 +23,8 @@
 // Measured (rocprofv3).  256 x 256: 8191x4096x4096 125-129 us, 2.2 PFLOP/s, MFMAs busy 0.52 of
 // the time; beside them a step's 72 copies take a CU's address unit about 480 ns and the operand
 // reads its LDS about 640 of the step's 1950.  Grouped, 12 rows an expert (32 x 256): first product
-// 652 us, 6.6 TB/s of weights; 48 rows (96 x 256): 770 us, 5.6 TB/s; each weight is read 1.00
-// times.  One row an expert (16 x 256): 108 us, 6.5 TB/s.
+// 655 us, 6.6 TB/s of weights; 48 rows (96 x 256): 805 us, 5.3 TB/s (MFMAs busy 0.30); each weight is
+// read 1.00 times.  One row an expert (16 x 256): 111 us, 6.4 TB/s.
 #include <atomic>
 #include <type_traits>
 

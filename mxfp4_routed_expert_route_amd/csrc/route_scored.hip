@@ -4,9 +4,10 @@
 // above, the routing kernel also writes the bit matrix and the expert-offsets kernels follow.
 //
 // Bound by the vector ALU: about 610 instructions a token (E = 256, softmax and bias), of which
-// the k + 1 rounds are a quarter.  8191 tokens take 12.2 us by the kernel trace (10.6 in a row of
-// calls); their 8.8 MB would need 1.7.  The one-launch form is one workgroup's chain of
-// dependent steps: 8 tokens of 256 experts routed and grouped in 7.2 us.
+// the k + 1 rounds are a quarter.  8191 tokens take 11.6 us by the kernel trace (10.9 to 12.0 in a
+// row of calls); their 8.8 MB would need 1.7.  Sigmoid scores in 8 groups take 14.0.  The one-launch
+// form is one workgroup's chain of dependent steps: 8 tokens of 256 experts routed and grouped, in
+// those groups, in 7.4 us.
 #include "group_core.h"
 #include "launch.h"
 #include "scored_core.h"
