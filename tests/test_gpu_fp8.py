@@ -645,3 +645,34 @@ def test_gemm_few_rows_of_very_many_columns(M, N, K, f32):
     if M > 3:
         test_gemm_beside_other_tensors(M, N, K, f32)
         test_gemm_infinite_scale_stays_in_its_row(M, N, K, f32)
+
+
+@pytest.mark.parametrize("E", [8, 1000])
+def test_ffn_at_the_activation_limit(E):
+    # x, h and y of 3.5 GiB as bf16: sampled rows, the last ones among them
+    from mxfp4_routed_expert_route_amd import binding
+    T, k, H, I = 3758096384 // 256, 1, 128, 128
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB")
+    say("ffn", T, E, k, H, I)
+    rng = np.random.default_rng(E)
+    d = ffn_inputs(rng, 16, E, k, H, I)
+    t = to_gpu(d)
+    g = torch.Generator(device="cuda").manual_seed(E)
+    x = torch.randn(T, H, device="cuda", generator=g).bfloat16()
+    ids = torch.randint(0, E, (T,), device="cuda", generator=g)
+    gather = torch.sort(ids, stable=True).indices.int()
+    counts = torch.bincount(ids, minlength=E).int()
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[1:] = counts.cumsum(0)
+    y = torch.full((T, H), -7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(binding.moe_fp8_workspace_bytes(T, E, k, H, I), dtype=torch.uint8, device="cuda")
+    binding.moe_grouped_ffn_fp8(x, k, t["w1"], t["w1s"], t["w2"], t["w2s"], counts, offsets, gather, 10.0, y, ws)
+    torch.cuda.synchronize()
+    ends = offsets.cpu().numpy().astype(np.int64)
+    for e in sorted({0, E // 2, E - 1}):
+        rows = np.unique(np.clip(np.concatenate([np.arange(40), ends[e + 1] - 40 + np.arange(40)]), ends[e], ends[e + 1] - 1))
+        token = gather[torch.from_numpy(rows).cuda()].long()
+        sub = dict(d, x=x[token].view(torch.int16).cpu().numpy().view(np.uint16), gather=np.arange(rows.size, dtype=np.int32),
+                   offsets=np.where(np.arange(E + 1) > e, rows.size, 0).astype(np.int32))
+        ffn_close(y[torch.from_numpy(rows).cuda()].float().cpu().numpy().astype(np.float64), sub, 10.0)
