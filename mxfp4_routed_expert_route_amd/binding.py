@@ -23,7 +23,10 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARGUMENT", 2: "MOE_ERR_UNSUPPORTED",
 EXPORTS = ("moe_route", "moe_build_bitmatrix", "moe_expert_offsets", "moe_route_and_group",
            "moe_grouped_ffn_mxfp4", "moe_combine", "moe_workspace_bytes", "moe_status_string",
            "moe_route_scored", "moe_route_scored_and_group", "moe_quantize_fp8", "moe_gemm_fp8",
-           "moe_gemm_fp8_workspace_bytes", "moe_grouped_ffn_fp8", "moe_fp8_workspace_bytes")
+           "moe_gemm_fp8_workspace_bytes", "moe_grouped_ffn_fp8", "moe_fp8_workspace_bytes",
+           "moe_rms_norm", "moe_rms_norm_grad", "moe_rms_norm_grad_workspace_bytes",
+           "moe_balance_loss", "moe_balance_loss_grad", "moe_balance_loss_workspace_bytes",
+           "moe_lora_group", "moe_lora_add", "moe_lora_add_workspace_bytes")
 
 
 # bf16 buffers may be given as bfloat16 tensors or as int16 tensors of bit patterns
@@ -69,6 +72,18 @@ _SIG = {
     "moe_grouped_ffn_fp8": [_P, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P, _P,
                             ctypes.c_float, _P, _P, ctypes.c_size_t, _P],
     "moe_fp8_workspace_bytes": [_I64, _I32, _I32, _I32, _I32],
+    "moe_rms_norm": [_P, _I64, _P, _I64, _I32, _I32, _P, ctypes.c_float, _P, _P, _P, _P, _P],
+    "moe_rms_norm_grad": [_P, _I64, _I64, _I32, _I32, _P, ctypes.c_float, _P, _P, _P, _P, _P,
+                          ctypes.c_size_t, _P],
+    "moe_rms_norm_grad_workspace_bytes": [_I64, _I32],
+    "moe_balance_loss": [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _I32, _P, _P, _P, _P, _P, _P,
+                         ctypes.c_size_t, _P],
+    "moe_balance_loss_grad": [_P, _I32, _I64, _I32, _I32, _I32, _P, _I32, _P, _P, _P, _P, _P],
+    "moe_balance_loss_workspace_bytes": [_I64, _I32, _I32],
+    "moe_lora_group": [_P, _I64, _I32, _P, _P, _P],
+    "moe_lora_add": [_P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _P, _P, _P, _P, _I32, _P, _I64, _P,
+                     _I64, _P, ctypes.c_size_t, _P],
+    "moe_lora_add_workspace_bytes": [_I64, _I32, _I32, _I32, _I32],
     "moe_workspace_bytes": [_I64, _I32, _I32, _I32, _I32],
     "moe_status_string": [ctypes.c_int],
 }
@@ -87,7 +102,9 @@ def load(path: str = LIB_PATH):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
-    for name in ("moe_workspace_bytes", "moe_gemm_fp8_workspace_bytes", "moe_fp8_workspace_bytes"):
+    for name in ("moe_workspace_bytes", "moe_gemm_fp8_workspace_bytes", "moe_fp8_workspace_bytes",
+                 "moe_rms_norm_grad_workspace_bytes", "moe_balance_loss_workspace_bytes",
+                 "moe_lora_add_workspace_bytes"):
         getattr(lib, name).restype = ctypes.c_size_t
     lib.moe_status_string.restype = ctypes.c_char_p
     _lib = lib
@@ -463,3 +480,164 @@ def moe_grouped_ffn_fp8(x, k: int, w1, w1_scale, w2, w2_scale, counts, offsets, 
          _arg(counts, _I32, (E,), dev, "counts"), _arg(offsets, _I32, (E + 1,), dev, "offsets"),
          _arg(gather, _I32, (T * k,), dev, "gather"), swiglu_limit,
          _arg(y_sorted, BF16, (T * k, H), dev, "y_sorted"), *_ws(ws, dev))
+
+
+# ------------------------------------------------------------ around the routed layer
+
+_FLOATS = {torch.float32: 0, torch.bfloat16: 1, torch.int16: 1}
+
+
+def _kind(t, name):
+    kind = None if t is None else _FLOATS.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {None if t is None else t.dtype}")
+    return kind
+
+
+def _of_kind(kind):
+    return BF16 if kind else _F32
+
+
+def _rows(t, dtypes, shape, dev, name):
+    """Pointer and row stride of a matrix whose rows are contiguous, checked like _arg's."""
+    if t is None or t.is_contiguous() or t.dim() != 2 or t.stride(1) != 1 or t.shape != shape:
+        return _arg(t, dtypes, shape, dev, name), shape[1]
+    if t.dtype not in dtypes or t.get_device() != dev or dev < 0:
+        _arg(t, dtypes, shape, dev, name)   # raises
+    return t.data_ptr(), t.stride(0)
+
+
+def _opt(t, dtypes, shape, dev, name):
+    return None if t is None else _arg(t, dtypes, shape, dev, name)
+
+
+def moe_rms_norm(x, weight, eps: float, *, residual=None, sum=None, y=None, q=None, scale=None,
+                 stream=None):
+    """RMS norm of s = bf16(x + residual) (or x), bf16 rows x [rows, H] (their stride may be more than
+    H): y [rows, H] in bf16, or q [rows, H] in E4M3 with scale [rows, ceil(H / 128)], or both; s goes
+    to sum.  weight [H] is fp32 or bf16."""
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, H]")
+    rows, H = x.shape
+    if H >= _END32:
+        _refuse_past_32_bits(H=H)
+    dev, kind = x.get_device(), _kind(weight, "weight")
+    ptr, stride = _rows(x, BF16, (rows, H), dev, "x")
+    _run("moe_rms_norm", dev, stream, ptr, stride, _opt(residual, BF16, (rows, H), dev, "residual"),
+         rows, H, kind, _arg(weight, _of_kind(kind), (H,), dev, "weight"), eps,
+         _opt(sum, BF16, (rows, H), dev, "sum"), _opt(y, BF16, (rows, H), dev, "y"),
+         _opt(q, E4M3, (rows, H), dev, "q"), _opt(scale, _F32, (rows, _runs(H)), dev, "scale"))
+
+
+def moe_rms_norm_grad_workspace_bytes(rows: int, H: int) -> int:
+    if not _sizes(rows, H):
+        return 0
+    return int(load().moe_rms_norm_grad_workspace_bytes(rows, H))
+
+
+def moe_rms_norm_grad(s, weight, eps: float, dy, dx, dweight, ws, *, dsum=None, stream=None):
+    """Gradient of moe_rms_norm's y: dx [rows, H] bf16 by s (moe_rms_norm's sum, or x without a
+    residual), with the gradient dsum that reaches s beside the norm, and dweight [H] fp32.  Either
+    of dx and dweight may be None; ws holds moe_rms_norm_grad_workspace_bytes(rows, H) bytes."""
+    if s.dim() != 2:
+        raise ValueError("s must be [rows, H]")
+    rows, H = s.shape
+    if H >= _END32:
+        _refuse_past_32_bits(H=H)
+    dev, kind = s.get_device(), _kind(weight, "weight")
+    ptr, stride = _rows(s, BF16, (rows, H), dev, "s")
+    _run("moe_rms_norm_grad", dev, stream, ptr, stride, rows, H, kind,
+         _arg(weight, _of_kind(kind), (H,), dev, "weight"), eps, _arg(dy, BF16, (rows, H), dev, "dy"),
+         _opt(dsum, BF16, (rows, H), dev, "dsum"), _opt(dx, BF16, (rows, H), dev, "dx"),
+         _opt(dweight, _F32, (H,), dev, "dweight"), *_ws(ws, dev))
+
+
+def _balance(logits, k, score, seq_offsets, n_seqs):
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}, got {score!r}")
+    kind = LOGIT_TYPES.get(logits.dtype)
+    if kind is None:
+        raise ValueError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if not (E < _END32 and -_END32 <= k < _END32 and n_seqs < _END32):
+        _refuse_past_32_bits(E=E, k=k, n_seqs=n_seqs)
+    dev = logits.get_device()
+    return (T, E, dev, (logits.dtype,), (_arg(logits, _LOGITS, (T, E), dev, "logits"), kind, T, E, k, SCORES[score]),
+            _opt(seq_offsets, _I32, (n_seqs + 1,), dev, "seq_offsets"))
+
+
+def moe_balance_loss_workspace_bytes(T: int, E: int, n_seqs: int = 1) -> int:
+    if not _sizes(T, E, n_seqs):
+        return 0
+    return int(load().moe_balance_loss_workspace_bytes(T, E, n_seqs))
+
+
+def moe_balance_loss(logits, topk_ids, loss, counts, ws, *, score: str = "softmax", seq_offsets=None,
+                     dloss=None, dlogits=None, add_to=None, stream=None):
+    """The balance loss [n_seqs] of router logits [T, E] and their chosen topk_ids [T, k] over packed
+    sequences (seq_offsets [n_seqs + 1]; None: one of all tokens), and the experts' counts
+    [n_seqs, E]; with dlogits, in the same pass, its gradient times dloss [n_seqs], plus add_to.
+    ws holds moe_balance_loss_workspace_bytes(T, E, n_seqs) bytes."""
+    if topk_ids.dim() != 2 or loss.dim() != 1:
+        raise ValueError("topk_ids must be [T, k] and loss [n_seqs]")
+    k, S = topk_ids.shape[1], loss.shape[0]
+    T, E, dev, of, how, offsets = _balance(logits, k, score, seq_offsets, S)
+    _run("moe_balance_loss", dev, stream, *how, _arg(topk_ids, _I32, (T, k), dev, "topk_ids"), offsets, S,
+         _arg(loss, _F32, (S,), dev, "loss"), _arg(counts, _I32, (S, E), dev, "counts"),
+         _opt(dloss, _F32, (S,), dev, "dloss"), _opt(add_to, of, (T, E), dev, "add_to"),
+         _opt(dlogits, of, (T, E), dev, "dlogits"), *_ws(ws, dev))
+
+
+def moe_balance_loss_grad(logits, k: int, counts, dloss, dlogits, *, score: str = "softmax",
+                          seq_offsets=None, add_to=None, stream=None):
+    """moe_balance_loss's dlogits alone, from its counts."""
+    if dloss.dim() != 1:
+        raise ValueError("dloss must be [n_seqs]")
+    S = dloss.shape[0]
+    T, E, dev, of, how, offsets = _balance(logits, k, score, seq_offsets, S)
+    _run("moe_balance_loss_grad", dev, stream, *how, offsets, S, _arg(counts, _I32, (S, E), dev, "counts"),
+         _arg(dloss, _F32, (S,), dev, "dloss"), _opt(add_to, of, (T, E), dev, "add_to"),
+         _arg(dlogits, of, (T, E), dev, "dlogits"))
+
+
+def moe_lora_group(adapter, L: int, offsets, rows, stream=None):
+    """The rows of a batch in their adapters' order: adapter [M] is each row's adapter (outside
+    0 .. L-1: none); rows [M], with adapter a's from offsets[a] to offsets[a + 1]."""
+    if adapter.dim() != 1:
+        raise ValueError("adapter must be [M]")
+    M = adapter.shape[0]
+    if not -_END32 <= L < _END32:
+        _refuse_past_32_bits(L=L)
+    dev = adapter.get_device()
+    _run("moe_lora_group", dev, stream, _arg(adapter, _I32, (M,), dev, "adapter"), M, L,
+         _arg(offsets, _I32, (L + 1,), dev, "offsets"), _arg(rows, _I32, (M,), dev, "rows"))
+
+
+def moe_lora_add_workspace_bytes(M: int, N: int, K: int, R: int, L: int) -> int:
+    if not _sizes(M, N, K, R, L):
+        return 0
+    return int(load().moe_lora_add_workspace_bytes(M, N, K, R, L))
+
+
+def moe_lora_add(x, a, b, scaling, offsets, rows, base, y, ws, stream=None):
+    """y [M, N] (bf16 or fp32) = base + scaling[l] (x A_l^T) B_l^T for the rows of each adapter l, base
+    for the others; x [M, K], a [L, R, K] and b [L, N, R] are bf16, scaling [L] fp32 or None (1),
+    offsets and rows moe_lora_group's.  base may be None (0), or y itself.  x, base and y may have row
+    strides of their own; ws holds moe_lora_add_workspace_bytes(M, N, K, R, L) bytes."""
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [M, K], a [L, R, K] and b [L, N, R]")
+    M, K = x.shape
+    L, R, _ = a.shape
+    N = b.shape[1]
+    if not (K < _END32 and N < _END32 and R < _END32 and L < _END32):
+        _refuse_past_32_bits(K=K, N=N, R=R, L=L)
+    dev, kind = x.get_device(), _kind(y, "y")
+    xp, xs = _rows(x, BF16, (M, K), dev, "x")
+    bp, bs = (None, 0) if base is None else _rows(base, _of_kind(kind), (M, N), dev, "base")
+    yp, ys = _rows(y, _of_kind(kind), (M, N), dev, "y")
+    _run("moe_lora_add", dev, stream, xp, xs, M, K, N, R, L, _arg(a, BF16, (L, R, K), dev, "a"),
+         _arg(b, BF16, (L, N, R), dev, "b"), _opt(scaling, _F32, (L,), dev, "scaling"),
+         _arg(offsets, _I32, (L + 1,), dev, "offsets"), _arg(rows, _I32, (M,), dev, "rows"), kind, bp, bs,
+         yp, ys, *_ws(ws, dev))

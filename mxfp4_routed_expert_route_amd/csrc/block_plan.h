@@ -1,0 +1,36 @@
+// Sizes of the operators around the routed layer that the host checks and the launches share.
+#pragma once
+#include <cstddef>
+#include <cstdint>
+
+#include "config.h"
+
+namespace moe {
+
+constexpr int kMaxAdapters = 1024;
+constexpr int kMaxRank = 256;
+constexpr int kMaxSequences = 1 << 20;
+constexpr int kLoraMaxN = 1 << 24;
+
+// moe_rms_norm_grad: workgroups, each of which leaves one partial row of dweight.
+constexpr int kNormGradGroups = 512;
+inline int64_t norm_grad_groups(int64_t rows) { return rows < kNormGradGroups ? rows : kNormGradGroups; }
+
+// moe_balance_loss: tokens per workgroup.
+constexpr int kBalanceMinChunk = 8;
+inline int64_t balance_slots(int64_t T, int n_seqs) {
+  return (T + kBalanceMinChunk - 1) / kBalanceMinChunk + n_seqs;
+}
+
+// moe_lora_add: rows of partial inner sums, [splits of K][M], and the splits that fit them.
+constexpr int64_t kLoraPartialRows = 4096;
+constexpr int kLoraMaxSplits = 16;
+inline size_t lora_partial_rows(int64_t M) {
+  return static_cast<size_t>(M > kLoraPartialRows ? M : kLoraPartialRows);
+}
+inline int lora_max_splits(int64_t M) {
+  const int64_t s = static_cast<int64_t>(lora_partial_rows(M)) / M;   // M >= 1
+  return static_cast<int>(s < kLoraMaxSplits ? s : kLoraMaxSplits);
+}
+
+}  // namespace moe

@@ -4,10 +4,13 @@
 #include <climits>
 #include <cstdio>
 #include <cstdlib>
+#include <initializer_list>
 
+#include "../block_plan.h"
 #include "../config.h"
 #include "../fp8_plan.h"
 #include "../validate.h"
+#include "../validate_block.h"
 #include "../validate_fp8.h"
 
 using namespace moe;
@@ -185,6 +188,42 @@ int main() {
   expect("fp8 ffn T * k", ffn8(INT32_MAX, 1024, 1, 65536, 128, SIZE_MAX), MOE_ERR_UNSUPPORTED);
   expect("fp8 ffn misaligned", check_ffn_fp8(p4, 16, 128, 128, 4, 2, p, p, p, p, p, p, p, p, p, 1 << 20), MOE_ERR_MISALIGNED);
   if (failures == 0) std::printf("scored routing and fp8 checks ok\n");
+
+  // the operators around the layer, at the ends of their ranges
+  auto norm = [&](int64_t rows, int32_t H, int64_t stride, float eps) {
+    return check_rms_norm(p, stride, p, rows, H, MOE_BF16, p, eps, p, nullptr, p, p);
+  };
+  expect("norm ok", norm(INT32_MAX, kMaxDim, kMaxDim, 1e-6f), MOE_OK);
+  expect("norm largest int64 rows", norm(INT64_MAX, 16, 16, 0.f), MOE_ERR_UNSUPPORTED);
+  expect("norm least int64 rows", norm(INT64_MIN, 16, 16, 0.f), MOE_ERR_INVALID_ARGUMENT);
+  expect("norm largest H", norm(1, INT32_MAX, INT32_MAX, 0.f), MOE_ERR_UNSUPPORTED);
+  expect("norm largest stride", norm(1, 16, INT64_MAX, 0.f), MOE_ERR_UNSUPPORTED);
+  expect("norm least stride", norm(1, 16, INT64_MIN, 0.f), MOE_ERR_INVALID_ARGUMENT);
+  size_t bytes = 0;
+  expect("norm grad ws", norm_grad_workspace(INT32_MAX, kMaxDim, &bytes), MOE_OK);
+  if (bytes < static_cast<size_t>(norm_grad_groups(INT32_MAX)) * kMaxDim * 4) { std::printf("FAIL norm grad ws\n"); ++failures; }
+  expect("norm grad small ws", check_rms_norm_grad(p, kMaxDim, INT32_MAX, kMaxDim, MOE_F32, p, 0.f, p, nullptr, nullptr, p, p, bytes - 1), MOE_ERR_WORKSPACE_TOO_SMALL);
+  auto balance = [&](int64_t T, int32_t E, int32_t k, int32_t seqs) {
+    return check_balance(p, MOE_F32, T, E, k, MOE_SCORE_SIGMOID, p, p, seqs, p, p, p, p, p, p, SIZE_MAX);
+  };
+  expect("balance ok", balance(INT32_MAX / 8, kMaxE, 8, kMaxSequences), MOE_OK);
+  expect("balance T * k", balance(INT32_MAX / 8 + 1, kMaxE, 8, 1), MOE_ERR_UNSUPPORTED);
+  expect("balance largest int64 T", balance(INT64_MAX, kMaxE, 1, 1), MOE_ERR_UNSUPPORTED);
+  expect("balance sequences", balance(1, 2, 1, INT32_MAX), MOE_ERR_UNSUPPORTED);
+  expect("balance ws", balance_workspace(INT32_MAX, kMaxE, kMaxSequences, &bytes), MOE_OK);
+  expect("lora group ok", check_lora_group(p, INT32_MAX, kMaxAdapters, p, p), MOE_OK);
+  auto lora = [&](int64_t M, int32_t N, int32_t K, int32_t R, int32_t L) {
+    return check_lora_add(p, K, M, K, N, R, L, p, p, p, p, p, MOE_BF16, p, N, p, N, p, SIZE_MAX);
+  };
+  expect("lora ok", lora(INT32_MAX, kLoraMaxN, kMaxDim, kMaxRank, kMaxAdapters), MOE_OK);
+  expect("lora largest int64 M", lora(INT64_MAX, 16, 16, 8, 1), MOE_ERR_UNSUPPORTED);
+  expect("lora least int64 M", lora(INT64_MIN, 16, 16, 8, 1), MOE_ERR_INVALID_ARGUMENT);
+  expect("lora largest sizes", lora(1, INT32_MAX, INT32_MAX, INT32_MAX, INT32_MAX), MOE_ERR_UNSUPPORTED);
+  for (int64_t M : {int64_t{1}, int64_t{300}, kLoraPartialRows, kLoraPartialRows + 1, int64_t{INT32_MAX}})
+    if (static_cast<size_t>(lora_max_splits(M)) * static_cast<size_t>(M) > lora_partial_rows(M) || lora_max_splits(M) < 1) {
+      std::printf("FAIL lora splits\n");
+      ++failures;
+    }
 
   if (failures) return 1;
   std::printf("validate_check ok\n");

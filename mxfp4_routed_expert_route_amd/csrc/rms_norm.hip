@@ -1,0 +1,144 @@
+// RMS norm with the residual's addition; outputs in bf16, in E4M3 with run scales, or both.
+//
+// A row stays in registers from its one load to the stores.  With z = s w (exact in fp32 for
+// bf16 weights) and y = z rstd, rstd is the same for a whole run of 128, so the codes are
+// E4M3(448 z / max |z|): they do not wait for rstd and carry none of its rounding.  Only a run
+// whose y, or z, lies below the format's floor of 2^-100 is quantised from y.
+#include "block.h"
+#include "fp8_common.h"
+#include "norm_core.h"
+
+namespace moe {
+namespace {
+
+template <int T, int C, int W>
+__global__ __launch_bounds__(T * W) void rms_norm_kernel(NormArgs a) {
+  static_assert(T == 64 || W == 1, "a barrier is for one row");
+  __shared__ float lds[2][T / 64];
+  const int t = threadIdx.x % T;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * W + threadIdx.x / T;
+  if (row >= a.rows) return;   // uniform per row
+  const uint16_t* x = a.x + row * a.x_stride;
+  const int64_t at = row * a.H;
+  uint4 s[C];
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int col = 8 * (t + T * i);
+    s[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (col < a.H) s[i] = *reinterpret_cast<const uint4*>(x + col);
+  }
+  if (a.residual != nullptr) {   // uniform
+    uint4 r[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int col = 8 * (t + T * i);
+      r[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (col < a.H) r[i] = *reinterpret_cast<const uint4*>(a.residual + at + col);
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int col = 8 * (t + T * i);
+      float u[8], v[8];
+      unpack_bf16x8(s[i], u);
+      unpack_bf16x8(r[i], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] += v[j];
+      s[i] = pack_bf16x8(u);
+      if (a.sum != nullptr && col < a.H) *reinterpret_cast<uint4*>(a.sum + at + col) = s[i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    float u[8];
+    unpack_bf16x8(s[i], u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss = fmaf(u[j], u[j], ss);
+  }
+  ss = row_sum<T>(ss, lds[0]);
+  const float f = row_factor(ss, a.eps);
+  if (f != 1.0f) {   // uniform per row
+    ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      float u[8];
+      unpack_bf16x8(s[i], u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(u[j] * f, u[j] * f, ss);
+    }
+    ss = row_sum<T>(ss, lds[1]);
+  }
+  const float rstd = row_rstd(ss, a.H, a.eps, f);
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int col = 8 * (t + T * i);
+    const bool here = col < a.H;
+    float z[8], y[8], w[8];
+    unpack_bf16x8(s[i], z);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 0.f;
+    if (here) load_weight8(a.w, a.w_f32, col, w);
+    uint32_t m = 0;   // largest |z|, on the bits
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      z[j] = z[j] * f * w[j];
+      y[j] = z[j] * rstd;
+      const uint32_t b = __float_as_uint(z[j]) & 0x7FFFFFFFu;
+      m = b > m ? b : m;
+    }
+    if (a.y != nullptr && here) *reinterpret_cast<uint4*>(a.y + at + col) = pack_bf16x8(y);
+    if (a.q != nullptr) {   // uniform
+      m = row16_max_u32(m);
+      const float zmax = __uint_as_float(m);
+      float amax = zmax * rstd;
+      const bool finite = amax < __builtin_inff();   // false for NaN
+      amax = finite ? fmaxf(amax, 0x1p-100f) : 1.0f;
+      const bool direct = zmax >= 0x1p-100f && zmax * rstd >= 0x1p-100f && zmax < __builtin_inff();
+      const RunScale r = run_scale(direct ? zmax : amax);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) y[j] = run_quotient(direct ? z[j] : y[j], r);
+      uint2 o = make_uint2(pack_e4m3(y[0], y[1], y[2], y[3]), pack_e4m3(y[4], y[5], y[6], y[7]));
+      if (!finite) o.x = o.y = kNanCodes;
+      if (here) {
+        *reinterpret_cast<uint2*>(a.q + at + col) = o;
+        if ((t & 15) == 0)
+          a.scale[row * ((a.H + kFp8Block - 1) / kFp8Block) + col / kFp8Block] =
+              finite ? amax / 448.0f : __uint_as_float(0x7FC00000u);
+      }
+    }
+  }
+}
+
+template <int T, int C, int W>
+hipError_t launch(NormArgs a, hipStream_t stream) {
+  // a launch has fewer than 2^32 threads
+  const int64_t most = 1 << 21, rows = a.rows;
+  const int64_t runs = (a.H + kFp8Block - 1) / kFp8Block;
+  for (int64_t r = 0; r < rows; r += most) {
+    a.rows = rows - r < most ? rows - r : most;
+    rms_norm_kernel<T, C, W><<<dim3(static_cast<unsigned>((a.rows + W - 1) / W)), dim3(T * W), 0, stream>>>(a);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    a.x += most * a.x_stride;
+    if (a.residual) a.residual += most * a.H;
+    if (a.sum) a.sum += most * a.H;
+    if (a.y) a.y += most * a.H;
+    if (a.q) a.q += most * a.H, a.scale += most * runs;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
+  if (a.H <= 512) return launch<64, 1, 4>(a, stream);
+  if (a.H <= 1024) return launch<64, 2, 4>(a, stream);
+  if (a.H <= 2048) return launch<64, 4, 4>(a, stream);
+  if (a.H <= 4096) return launch<256, 2, 1>(a, stream);
+  if (a.H <= 8192) return launch<256, 4, 1>(a, stream);
+  if (a.H <= 16384) return launch<1024, 2, 1>(a, stream);
+  if (a.H <= 32768) return launch<1024, 4, 1>(a, stream);
+  return launch<1024, 8, 1>(a, stream);
+}
+
+}  // namespace moe
