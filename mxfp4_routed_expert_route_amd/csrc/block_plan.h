@@ -12,9 +12,14 @@ constexpr int kMaxRank = 256;
 constexpr int kMaxSequences = 1 << 20;
 constexpr int kLoraMaxN = 1 << 24;
 
-// moe_rms_norm_grad: workgroups, each of which leaves one partial row of dweight.
-constexpr int kNormGradGroups = 512;
-inline int64_t norm_grad_groups(int64_t rows) { return rows < kNormGradGroups ? rows : kNormGradGroups; }
+// moe_rms_norm_grad: most workgroups, each of which leaves one partial row of dweight: 2^18
+// threads, whose partial rows are 8 MB at most (16 beyond H = 16384).
+inline int64_t norm_grad_groups(int64_t rows, int H) {
+  int64_t threads = 256;   // of a row, or of several short ones
+  while (threads < 1024 && threads * 8 < H) threads *= 2;
+  const int64_t most = (1 << 18) / threads;
+  return rows < most ? rows : most;
+}
 
 // moe_balance_loss: tokens per workgroup.
 constexpr int kBalanceMinChunk = 8;

@@ -201,7 +201,7 @@ int main() {
   expect("norm least stride", norm(1, 16, INT64_MIN, 0.f), MOE_ERR_INVALID_ARGUMENT);
   size_t bytes = 0;
   expect("norm grad ws", norm_grad_workspace(INT32_MAX, kMaxDim, &bytes), MOE_OK);
-  if (bytes < static_cast<size_t>(norm_grad_groups(INT32_MAX)) * kMaxDim * 4) { std::printf("FAIL norm grad ws\n"); ++failures; }
+  if (bytes < static_cast<size_t>(norm_grad_groups(INT32_MAX, kMaxDim)) * kMaxDim * 4) { std::printf("FAIL norm grad ws\n"); ++failures; }
   expect("norm grad small ws", check_rms_norm_grad(p, kMaxDim, INT32_MAX, kMaxDim, MOE_F32, p, 0.f, p, nullptr, nullptr, p, p, bytes - 1), MOE_ERR_WORKSPACE_TOO_SMALL);
   auto balance = [&](int64_t T, int32_t E, int32_t k, int32_t seqs) {
     return check_balance(p, MOE_F32, T, E, k, MOE_SCORE_SIGMOID, p, p, seqs, p, p, p, p, p, p, SIZE_MAX);

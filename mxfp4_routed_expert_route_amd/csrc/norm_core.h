@@ -1,7 +1,9 @@
 // A row's statistics for the RMS norm and its gradient.
 //
-// Layout.  T lanes take a row; lane t holds elements 8 (t + T i) .. + 7 of chunk i, so a load is 16
-// bytes a lane and a run of 128 elements lies in 16 neighbouring lanes of one chunk.
+// Layout.  T threads take a row, thread t elements 8 (t + T i) .. + 7 of chunk i, so a load is 16
+// bytes a thread and a run of 128 elements lies in 16 neighbouring lanes of one chunk.  Rows of up
+// to 512 elements take 16, 32 or 64 lanes of a wavefront (kLanes) and need no barrier; longer
+// ones a workgroup of whole wavefronts (kLanes 0), as few threads as hold them.
 //
 // Range.  Squares of bf16 values leave fp32 beyond about 2^63 and below 2^-63.  A row whose sum of
 // squares is outside [2^-80, 2^100] is multiplied by a power of two and summed again; eps
@@ -12,17 +14,10 @@
 
 namespace moe {
 
-constexpr int kNormPower = 100;
-
-struct RowFactor {
-  float f;       // the row is multiplied by this power of two
-  double f2;
-};
-
 // What a row with the sum of squares `ss` is multiplied by; 1 for all but extreme rows.
-__device__ __forceinline__ float row_factor(float ss, float mean_eps_floor) {
+__device__ __forceinline__ float row_factor(float ss, float eps) {
   if (!(ss <= 0x1p100f)) return 0x1p-100f;
-  return ss < 0x1p-80f && mean_eps_floor < 0x1p-60f ? 0x1p100f : 1.0f;
+  return ss < 0x1p-80f && eps < 0x1p-60f ? 0x1p100f : 1.0f;
 }
 
 // 1 / sqrt(ss / H + eps f^2) of a row multiplied by f.
@@ -31,20 +26,33 @@ __device__ __forceinline__ float row_rstd(float ss, int H, float eps, float f) {
   return static_cast<float>(1.0 / sqrt(mean));
 }
 
-// Sum over a row's T lanes (one wavefront or a workgroup), in all of them.  `lds` holds T / 64
-// floats that no other sum since the last barrier has used.
-template <int T>
-__device__ __forceinline__ float row_sum(float v, float* lds) {
-  v = run_sum<64>(v);
-  if constexpr (T > 64) {
+constexpr int kMaxWaves = 16;   // of a workgroup
+
+// Sums of two values over a row's threads, in all of them.  A workgroup's go through `lds`, which no
+// thread may still be reading from for another sum.
+template <int kLanes>
+__device__ __forceinline__ float2 row_sum(float2 v, float2* lds) {
+  constexpr int L = kLanes ? kLanes : 64;
+  v.x = run_sum<L>(v.x);
+  v.y = run_sum<L>(v.y);
+  if constexpr (kLanes == 0) {
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < T / 64; ++i) v += lds[i];
+    const int waves = blockDim.x >> 6;
+    v = lds[0];
+    for (int i = 1; i < waves; ++i) {
+      const float2 o = lds[i];
+      v.x += o.x;
+      v.y += o.y;
+    }
   }
   return v;
 }
+
+// Lanes of a wavefront for a row of H <= 512 elements.
+inline int norm_lanes(int H) { return H <= 128 ? 16 : H <= 256 ? 32 : 64; }
+// Threads for a row of H elements in chunks of 8 C.
+inline int norm_threads(int H, int C) { return (H + 8 * 64 * C - 1) / (8 * 64 * C) * 64; }
 
 // Eight weights from element `at` on.
 __device__ __forceinline__ void load_weight8(const void* w, bool f32, int at, float (&v)[8]) {

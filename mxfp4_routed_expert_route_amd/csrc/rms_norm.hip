@@ -11,22 +11,23 @@
 namespace moe {
 namespace {
 
-template <int T, int C, int W>
-__global__ __launch_bounds__(T * W) void rms_norm_kernel(NormArgs a) {
-  static_assert(T == 64 || W == 1, "a barrier is for one row");
-  __shared__ float lds[2][T / 64];
-  const int t = threadIdx.x % T;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * W + threadIdx.x / T;
-  if (row >= a.rows) return;   // uniform per row
+template <int kLanes, int C>
+__global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs a) {
+  __shared__ float2 lds[2][kMaxWaves];
+  const int T = kLanes ? kLanes : blockDim.x;
+  const int t = kLanes ? threadIdx.x % kLanes : threadIdx.x;
+  const int64_t row = kLanes ? static_cast<int64_t>(blockIdx.x) * (256 / kLanes) + threadIdx.x / kLanes : blockIdx.x;
+  const bool live = row < a.rows;   // lanes without a row keep the others company
+  const int H = live ? a.H : 0;
   const uint16_t* x = a.x + row * a.x_stride;
   const int64_t at = row * a.H;
   uint4 s[C];
-  float ss = 0.f;
+  float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int col = 8 * (t + T * i);
     s[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (col < a.H) s[i] = *reinterpret_cast<const uint4*>(x + col);
+    if (col < H) s[i] = *reinterpret_cast<const uint4*>(x + col);
   }
   if (a.residual != nullptr) {   // uniform
     uint4 r[C];
@@ -34,7 +35,7 @@ __global__ __launch_bounds__(T * W) void rms_norm_kernel(NormArgs a) {
     for (int i = 0; i < C; ++i) {
       const int col = 8 * (t + T * i);
       r[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (col < a.H) r[i] = *reinterpret_cast<const uint4*>(a.residual + at + col);
+      if (col < H) r[i] = *reinterpret_cast<const uint4*>(a.residual + at + col);
     }
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -45,7 +46,7 @@ __global__ __launch_bounds__(T * W) void rms_norm_kernel(NormArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) u[j] += v[j];
       s[i] = pack_bf16x8(u);
-      if (a.sum != nullptr && col < a.H) *reinterpret_cast<uint4*>(a.sum + at + col) = s[i];
+      if (a.sum != nullptr && col < H) *reinterpret_cast<uint4*>(a.sum + at + col) = s[i];
     }
   }
 #pragma unroll
@@ -53,26 +54,26 @@ __global__ __launch_bounds__(T * W) void rms_norm_kernel(NormArgs a) {
     float u[8];
     unpack_bf16x8(s[i], u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) ss = fmaf(u[j], u[j], ss);
+    for (int j = 0; j < 8; ++j) ss.x = fmaf(u[j], u[j], ss.x);
   }
-  ss = row_sum<T>(ss, lds[0]);
-  const float f = row_factor(ss, a.eps);
-  if (f != 1.0f) {   // uniform per row
-    ss = 0.f;
+  ss = row_sum<kLanes>(ss, lds[0]);
+  const float f = row_factor(ss.x, a.eps);
+  if (f != 1.0f) {   // uniform over the threads of a row
+    ss.x = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float u[8];
       unpack_bf16x8(s[i], u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(u[j] * f, u[j] * f, ss);
+      for (int j = 0; j < 8; ++j) ss.x = fmaf(u[j] * f, u[j] * f, ss.x);
     }
-    ss = row_sum<T>(ss, lds[1]);
+    ss = row_sum<kLanes>(ss, lds[1]);
   }
-  const float rstd = row_rstd(ss, a.H, a.eps, f);
+  const float rstd = row_rstd(ss.x, a.H, a.eps, f);
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int col = 8 * (t + T * i);
-    const bool here = col < a.H;
+    const bool here = col < H;
     float z[8], y[8], w[8];
     unpack_bf16x8(s[i], z);
 #pragma unroll
@@ -109,14 +110,17 @@ __global__ __launch_bounds__(T * W) void rms_norm_kernel(NormArgs a) {
   }
 }
 
-template <int T, int C, int W>
+template <int kLanes, int C>
 hipError_t launch(NormArgs a, hipStream_t stream) {
+  const int per = kLanes ? 256 / kLanes : 1;   // rows of a workgroup
+  const int threads = kLanes ? 256 : norm_threads(a.H, C);
   // a launch has fewer than 2^32 threads
   const int64_t most = 1 << 21, rows = a.rows;
   const int64_t runs = (a.H + kFp8Block - 1) / kFp8Block;
   for (int64_t r = 0; r < rows; r += most) {
     a.rows = rows - r < most ? rows - r : most;
-    rms_norm_kernel<T, C, W><<<dim3(static_cast<unsigned>((a.rows + W - 1) / W)), dim3(T * W), 0, stream>>>(a);
+    rms_norm_kernel<kLanes, C>
+        <<<dim3(static_cast<unsigned>((a.rows + per - 1) / per)), dim3(threads), 0, stream>>>(a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     a.x += most * a.x_stride;
@@ -131,14 +135,19 @@ hipError_t launch(NormArgs a, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
-  if (a.H <= 512) return launch<64, 1, 4>(a, stream);
-  if (a.H <= 1024) return launch<64, 2, 4>(a, stream);
-  if (a.H <= 2048) return launch<64, 4, 4>(a, stream);
-  if (a.H <= 4096) return launch<256, 2, 1>(a, stream);
-  if (a.H <= 8192) return launch<256, 4, 1>(a, stream);
-  if (a.H <= 16384) return launch<1024, 2, 1>(a, stream);
-  if (a.H <= 32768) return launch<1024, 4, 1>(a, stream);
-  return launch<1024, 8, 1>(a, stream);
+  if (a.H <= 512) {
+    switch (norm_lanes(a.H)) {
+      case 16: return launch<16, 1>(a, stream);
+      case 32: return launch<32, 1>(a, stream);
+      default: return launch<64, 1>(a, stream);
+    }
+  }
+  // chunks a thread, 1 / 2: 8191 x 1024 18.8 us / 17.4, 8191 x 2048 31.9 / 32.5, 8191 x 4096 59.1 /
+  // 56.9, 4096 x 8192 65.7 / 58.4; 4 are slower (60.6 at 8191 x 4096)
+  if (a.H <= 2048) return launch<0, 1>(a, stream);
+  if (a.H <= 16384) return launch<0, 2>(a, stream);
+  if (a.H <= 32768) return launch<0, 4>(a, stream);
+  return launch<0, 8>(a, stream);
 }
 
 }  // namespace moe

@@ -11,147 +11,178 @@
 namespace moe {
 namespace {
 
-template <int T, int C, int W>
-__global__ __launch_bounds__(T * W) void norm_grad_kernel(NormGradArgs a) {
-  static_assert(T == 64 || W == 1, "a barrier is for one row");
-  __shared__ float sums[4][T / 64];
-  __shared__ float part[W > 1 ? W * 64 * 8 : 1];
-  const int t = threadIdx.x % T, wave = threadIdx.x / T;
-  float acc[C][8];
+// What a thread holds of a row; from C = 4 on a row is read twice instead, the second time from cache.
+template <int C>
+struct GradRow {
+  uint4 s[C], g[C], e[C];   // s, dy, dsum
+};
+
+template <int kLanes, int C>
+__global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_grad_kernel(NormGradArgs a) {
+  constexpr int kRows = kLanes ? 256 / kLanes : 1;   // of a workgroup at a time
+  constexpr bool kKeep = C <= 2;   // the row, and the weights
+  __shared__ float2 sums[3][kMaxWaves];
+  __shared__ float part[kLanes ? 256 * 8 : 1];
+  const int T = kLanes ? kLanes : blockDim.x;
+  const int t = kLanes ? threadIdx.x % kLanes : threadIdx.x;
+  const int sub = kLanes ? threadIdx.x / kLanes : 0;
+  float weights[kKeep ? C : 1][8], acc[C][8];
 #pragma unroll
   for (int i = 0; i < C; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * W;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * W + wave; row < a.rows; row += step) {
-    const uint16_t* s_row = a.s + row * a.s_stride;
-    const int64_t at = row * a.H;
-    uint4 s[C], g[C];
+  auto load_weights = [&](int i, float (&w)[8]) {
+    const int col = 8 * (t + T * i);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = 0.f;
+    if (col < a.H) load_weight8(a.w, a.w_f32, col, w);
+  };
+  if constexpr (kKeep)
+#pragma unroll
+    for (int i = 0; i < C; ++i) load_weights(i, weights[i]);
+  auto load = [&](int64_t row, int i, uint4& s, uint4& g, uint4& e) {
+    const int col = 8 * (t + T * i);
+    s = g = e = make_uint4(0u, 0u, 0u, 0u);
+    if (row < a.rows && col < a.H) {
+      s = *reinterpret_cast<const uint4*>(a.s + row * a.s_stride + col);
+      g = *reinterpret_cast<const uint4*>(a.dy + row * a.H + col);
+      if (a.dsum != nullptr) e = *reinterpret_cast<const uint4*>(a.dsum + row * a.H + col);
+    }
+  };
+  // chunk i of the row: s, dy, dsum, w
+  auto chunk = [&](const GradRow<C>& r, int64_t row, int i, float (&u)[8], float (&d)[8], float (&e)[8], float (&w)[8]) {
+    if constexpr (kKeep) {
+      unpack_bf16x8(r.s[i], u);
+      unpack_bf16x8(r.g[i], d);
+      unpack_bf16x8(r.e[i], e);
+    } else {
+      uint4 s4, g4, e4;
+      load(row, i, s4, g4, e4);
+      unpack_bf16x8(s4, u);
+      unpack_bf16x8(g4, d);
+      unpack_bf16x8(e4, e);
+    }
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = weights[i][j];
+    } else {
+      load_weights(i, w);
+    }
+  };
+  auto both = [&](const GradRow<C>& r, int64_t row, float f) {
+    float2 v = make_float2(0.f, 0.f);   // of s^2, of z s
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-      const int col = 8 * (t + T * i);
-      s[i] = g[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (col < a.H) {
-        s[i] = *reinterpret_cast<const uint4*>(s_row + col);
-        g[i] = *reinterpret_cast<const uint4*>(a.dy + at + col);
-      }
-    }
-    auto both = [&](float f, float& ss, float& dot) {
-      ss = dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < C; ++i) {
-        const int col = 8 * (t + T * i);
-        float u[8], d[8], w[8];
-        unpack_bf16x8(s[i], u);
-        unpack_bf16x8(g[i], d);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 0.f;
-        if (col < a.H) load_weight8(a.w, a.w_f32, col, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          u[j] *= f;
-          ss = fmaf(u[j], u[j], ss);
-          dot = fmaf(d[j] * w[j], u[j], dot);
-        }
-      }
-    };
-    float ss, dot;
-    both(1.0f, ss, dot);
-    ss = row_sum<T>(ss, sums[0]);
-    dot = row_sum<T>(dot, sums[1]);
-    const float f = row_factor(ss, a.eps);
-    if (f != 1.0f) {   // uniform per row
-      both(f, ss, dot);
-      ss = row_sum<T>(ss, sums[2]);
-      dot = row_sum<T>(dot, sums[3]);
-    }
-    if constexpr (T > 64) __syncthreads();   // the next row's sums
-    const float r = row_rstd(ss, a.H, a.eps, f);
-    const float c = r * dot / static_cast<float>(a.H);   // mean(z u)
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      const int col = 8 * (t + T * i);
-      if (col >= a.H) continue;
-      float u[8], d[8], w[8];
-      unpack_bf16x8(s[i], u);
-      unpack_bf16x8(g[i], d);
-      load_weight8(a.w, a.w_f32, col, w);
+      float u[8], d[8], e[8], w[8];
+      chunk(r, row, i, u, d, e, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        u[j] = u[j] * f * r;
-        acc[i][j] = fmaf(d[j], u[j], acc[i][j]);
-        d[j] = f * r * fmaf(-u[j], c, d[j] * w[j]);
+        u[j] *= f;
+        v.x = fmaf(u[j], u[j], v.x);
+        v.y = fmaf(d[j] * w[j], u[j], v.y);
       }
-      if (a.dx != nullptr) {   // uniform
-        if (a.dsum != nullptr) {
-          float e[8];
-          unpack_bf16x8(*reinterpret_cast<const uint4*>(a.dsum + at + col), e);
+    }
+    return v;
+  };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kRows;
+  int turn = 0;
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRows; row0 < a.rows; row0 += step) {   // uniform
+    const int64_t row = row0 + sub;
+    GradRow<C> r;
+    if constexpr (kKeep)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] += e[j];
-        }
-        *reinterpret_cast<uint4*>(a.dx + at + col) = pack_bf16x8(d);
+      for (int i = 0; i < C; ++i) load(row, i, r.s[i], r.g[i], r.e[i]);
+    float2 v = row_sum<kLanes>(both(r, row, 1.0f), sums[turn]);   // two in turn: one barrier a row
+    turn ^= 1;
+    const float f = row_factor(v.x, a.eps);
+    if (f != 1.0f) {   // uniform over the threads of a row
+      v = row_sum<kLanes>(both(r, row, f), sums[2]);
+      if constexpr (kLanes == 0) __syncthreads();   // sums[2] may be next in line too
+    }
+    const float rstd = row_rstd(v.x, a.H, a.eps, f);
+    const float c = rstd * v.y / static_cast<float>(a.H);   // mean(z u)
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      const int col = 8 * (t + T * i);
+      float u[8], d[8], e[8], w[8];
+      chunk(r, row, i, u, d, e, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        u[j] = u[j] * f * rstd;
+        acc[i][j] = fmaf(d[j], u[j], acc[i][j]);
+        d[j] = fmaf(f * rstd, fmaf(-u[j], c, d[j] * w[j]), e[j]);
       }
+      if (a.dx != nullptr && row < a.rows && col < a.H)
+        *reinterpret_cast<uint4*>(a.dx + row * a.H + col) = pack_bf16x8(d);
     }
   }
   if (a.dw == nullptr) return;
   float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.H;
+  if constexpr (kLanes == 0) {
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int col = 8 * (t + T * i);
-    if constexpr (W == 1) {
+    for (int i = 0; i < C; ++i) {
+      const int col = 8 * (t + T * i);
       if (col < a.H) {
         *reinterpret_cast<float4*>(out + col) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
         *reinterpret_cast<float4*>(out + col + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
       }
-    } else {
-      __syncthreads();
+    }
+  } else {   // the rows' sums at element 8 t + j: [row][j][t]
 #pragma unroll
-      for (int j = 0; j < 8; ++j) part[(wave * 8 + j) * 64 + t] = acc[i][j];
-      __syncthreads();
-      for (int e = threadIdx.x; e < 512; e += T * W) {   // element 8 (e % 64) + e / 64 of the chunk
-        float v = 0.f;
+    for (int j = 0; j < 8; ++j) part[(sub * 8 + j) * kLanes + t] = acc[0][j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < 8 * kLanes; e += 256) {
+      float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < W; ++k) v += part[k * 512 + e];
-        const int to = 8 * ((e & 63) + 64 * i) + (e >> 6);
-        if (to < a.H) out[to] = v;
-      }
+      for (int k = 0; k < kRows; ++k) v += part[k * 8 * kLanes + e];
+      const int to = 8 * (e % kLanes) + e / kLanes;
+      if (to < a.H) out[to] = v;
     }
   }
 }
 
-// dweight: 64 columns a workgroup, the partial rows dealt to 16 groups of 16 lanes.
-__global__ __launch_bounds__(256) void norm_grad_sum_kernel(const float* __restrict__ part, int groups, int H,
-                                                            float* __restrict__ dw) {
-  __shared__ float4 lds[16][16];
-  const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
-  const int col = 64 * blockIdx.x + 4 * lane;
+// dweight: 32 columns a workgroup, the partial rows dealt to 128 groups of 8 lanes.
+__global__ __launch_bounds__(1024) void norm_grad_sum_kernel(const float* __restrict__ part, int groups, int H,
+                                                             float* __restrict__ dw) {
+  __shared__ float4 lds[128][8];
+  const int lane = threadIdx.x & 7, group = threadIdx.x >> 3;
+  const int col = 32 * blockIdx.x + 4 * lane;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (col < H)   // H is a multiple of 8
-    for (int p = group; p < groups; p += 16) {
-      const float4 o = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(p) * H + col);
-      v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+  auto add = [&](float4 o) { v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w; };
+  if (col < H) {   // H is a multiple of 8
+    const float* p = part + col;
+    int i = group;
+    for (; i + 384 < groups; i += 512) {   // four loads on their way at once
+      float4 o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = *reinterpret_cast<const float4*>(p + static_cast<int64_t>(i + 128 * k) * H);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) add(o[k]);
     }
+    for (; i < groups; i += 128) add(*reinterpret_cast<const float4*>(p + static_cast<int64_t>(i) * H));
+  }
   lds[group][lane] = v;
   __syncthreads();
-  if (group != 0 || col >= H) return;
+  if (threadIdx.x >= 64) return;   // one wavefront: groups 0 .. 7
 #pragma unroll
-  for (int i = 1; i < 16; ++i) {
-    const float4 o = lds[i][lane];
-    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-  }
-  *reinterpret_cast<float4*>(dw + col) = v;
+  for (int i = 1; i < 16; ++i) add(lds[group + 8 * i][lane]);
+#pragma unroll
+  for (int d = 8; d <= 32; d *= 2)
+    add(make_float4(__shfl_xor(v.x, d, 64), __shfl_xor(v.y, d, 64), __shfl_xor(v.z, d, 64), __shfl_xor(v.w, d, 64)));
+  if (group == 0 && col < H) *reinterpret_cast<float4*>(dw + col) = v;
 }
 
-template <int T, int C, int W>
+template <int kLanes, int C>
 hipError_t launch(const NormGradArgs& a, hipStream_t stream) {
-  const int64_t need = (a.rows + W - 1) / W;
-  const int groups = static_cast<int>(need < kNormGradGroups ? need : kNormGradGroups);
+  const int threads = kLanes ? 256 : norm_threads(a.H, C), per = kLanes ? 256 / kLanes : 1;
+  const int64_t need = (a.rows + per - 1) / per, most = norm_grad_groups(a.rows, a.H);
+  const int groups = static_cast<int>(need < most ? need : most);
   if (groups > 0) {
-    norm_grad_kernel<T, C, W><<<dim3(groups), dim3(T * W), 0, stream>>>(a);
+    norm_grad_kernel<kLanes, C><<<dim3(groups), dim3(threads), 0, stream>>>(a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess || a.dw == nullptr) return err;
   }
-  norm_grad_sum_kernel<<<dim3((a.H + 63) / 64), dim3(256), 0, stream>>>(a.part, groups, a.H, a.dw);
+  norm_grad_sum_kernel<<<dim3((a.H + 31) / 32), dim3(1024), 0, stream>>>(a.part, groups, a.H, a.dw);
   return hipGetLastError();
 }
 
@@ -159,14 +190,19 @@ hipError_t launch(const NormGradArgs& a, hipStream_t stream) {
 
 hipError_t launch_rms_norm_grad(const NormGradArgs& a, hipStream_t stream) {
   if (a.rows == 0 && a.dw == nullptr) return hipSuccess;
-  if (a.H <= 512) return launch<64, 1, 4>(a, stream);
-  if (a.H <= 1024) return launch<64, 2, 4>(a, stream);
-  if (a.H <= 2048) return launch<64, 4, 4>(a, stream);
-  if (a.H <= 4096) return launch<64, 8, 4>(a, stream);
-  if (a.H <= 8192) return launch<256, 4, 1>(a, stream);
-  if (a.H <= 16384) return launch<1024, 2, 1>(a, stream);
-  if (a.H <= 32768) return launch<1024, 4, 1>(a, stream);
-  return launch<1024, 8, 1>(a, stream);
+  if (a.H <= 512) {
+    switch (norm_lanes(a.H)) {
+      case 16: return launch<16, 1>(a, stream);
+      case 32: return launch<32, 1>(a, stream);
+      default: return launch<64, 1>(a, stream);
+    }
+  }
+  // chunks a thread, 1 / 2: 8191 x 1024 27.2 us / 29.1, 8191 x 2048 34.8 / 38.0, 8191 x 4096 56.7 / 56.6,
+  // 4096 x 8192 64.7 / 61.0; the next row on its way while one is worked on gains nothing (57.4 / 56.2)
+  if (a.H <= 4096) return launch<0, 1>(a, stream);
+  if (a.H <= 16384) return launch<0, 2>(a, stream);
+  if (a.H <= 32768) return launch<0, 4>(a, stream);
+  return launch<0, 8>(a, stream);
 }
 
 }  // namespace moe

@@ -59,7 +59,7 @@ moe_status check_rms_norm(const void* x, int64_t x_stride, const void* residual,
 moe_status norm_grad_workspace(int64_t rows, int32_t H, size_t* bytes) {
   const moe_status s = check_rows(rows, H, 8);
   if (s != MOE_OK) return s;
-  *bytes = align_up(static_cast<size_t>(norm_grad_groups(rows)) * static_cast<size_t>(H) * sizeof(float), 256);
+  *bytes = align_up(static_cast<size_t>(norm_grad_groups(rows, H)) * static_cast<size_t>(H) * sizeof(float), 256);
   return MOE_OK;
 }
 
