@@ -28,10 +28,10 @@ inline int64_t balance_slots(int64_t T, int n_seqs) {
 }
 
 // moe_lora_add: rows of partial inner sums, [splits of K][M], and the splits that fit them.
-constexpr int64_t kLoraPartialRows = 4096;
+constexpr int64_t kLoraPartialRows = 8192;
 constexpr int kLoraMaxSplits = 16;
-inline size_t lora_partial_rows(int64_t M) {
-  return static_cast<size_t>(M > kLoraPartialRows ? M : kLoraPartialRows);
+inline size_t lora_partial_rows(int64_t M) {   // two splits at least
+  return static_cast<size_t>(2 * M > kLoraPartialRows ? 2 * M : kLoraPartialRows);
 }
 inline int lora_max_splits(int64_t M) {
   const int64_t s = static_cast<int64_t>(lora_partial_rows(M)) / M;   // M >= 1

@@ -30,6 +30,7 @@
 
 #include "fp8.h"
 #include "fp8_common.h"
+#include "lds_copy.h"
 
 namespace moe {
 namespace {
@@ -62,21 +63,6 @@ __device__ __forceinline__ void copy4(i32x4 rsrc, uint32_t voff, uint32_t soff, 
   asm volatile("s_nop 0\n\tbuffer_load_dword %0, %1, %2 offen lds"
                :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
 }
-template <int kLeft>
-__device__ __forceinline__ void wait_copies() {
-  static_assert(kLeft < 64, "the counter's range");
-  // vmcnt in bits 3:0 and 15:14, the other counters at their maximum (no wait)
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((kLeft & 15) | ((kLeft >> 4) << 14) | 0x0F70);
-  asm volatile("" ::: "memory");
-}
-__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
-__device__ __forceinline__ void barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // Non-temporal: with ordinary stores, the second product of 12,288 rows x 4096 columns (100 MB
 // out, 2.1 GB of weights in) takes 436 us, with these 406.
 __device__ __forceinline__ void store16(void* p, i32x4 v) {

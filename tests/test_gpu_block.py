@@ -556,6 +556,24 @@ def test_lora_add(M, N, K, R, L, dtype):
     check_lora(x, a, b, s, ids, base, run_lora(x, a, b, s, ids, base, dtype))
 
 
+@pytest.mark.parametrize("M,N,K,R,L", [(6500, 72, 64, 16, 1), (7000, 100, 72, 40, 3), (8191, 64, 136, 64, 8), (6300, 130, 1032, 24, 2),
+                                       (20000, 65, 64, 8, 5), (9000, 33, 8, 64, 9), (7777, 264, 520, 32, 4), (40000, 16, 64, 48, 200)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("packed", [False, True])
+def test_lora_add_many_rows(M, N, K, R, L, dtype, packed):
+    r = np.random.default_rng(M + N + R)
+    ids = r.integers(-1, L, size=M)
+    if packed:      # requests of different lengths, in the batch's order
+        cuts = np.sort(r.integers(0, M, size=2 * L))
+        ids = r.integers(-1, L, size=2 * L + 1)[np.searchsorted(cuts, np.arange(M), side="right")]
+    x, a, b, s, base = lora(M, N, K, R, L, ids, M + K, dtype)
+    y = run_lora(x, a, b, s, ids, base, dtype)
+    check_lora(x, a, b, s, ids, base, y)
+    place = base.clone()
+    assert torch.equal(run_lora(x, a, b, s, ids, place, dtype, place), y)
+    check_lora(x, a, b, s, ids, None, run_lora(x, a, b, s, ids, None, dtype))
+
+
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("M", [1, 7, 130, 600])
 def test_lora_base_in_place_and_without(M, dtype):
@@ -601,17 +619,18 @@ def test_lora_infinite_inner_sums_stay_infinite():
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-def test_lora_on_slices_of_wider_rows(dtype):
+@pytest.mark.parametrize("M", [61, 700, 7000])
+def test_lora_on_slices_of_wider_rows(dtype, M):
     """The adapters of one of several projections whose results share rows."""
     r = np.random.default_rng(5)
-    ids = r.integers(-1, 4, size=61)
-    x, a, b, s, _ = lora(61, 136, 128, 16, 4, ids, 6, dtype)
-    wide_x, wide = randn(gen(7), 61, 200), randn(gen(8), 61, 408, dtype=dtype)
+    ids = r.integers(-1, 4, size=M)
+    x, a, b, s, _ = lora(M, 136, 128, 16, 4, ids, 6, dtype)
+    wide_x, wide = randn(gen(7), M, 200), randn(gen(8), M, 408, dtype=dtype)
     xs, ys = wide_x[:, 64:192], wide[:, 136:272]
     before = wide.clone()
     check_lora(xs, a, b, s, ids, before[:, 136:272], run_lora(xs, a, b, s, ids, ys, dtype, ys))
     assert torch.equal(wide[:, :136], before[:, :136]) and torch.equal(wide[:, 272:], before[:, 272:])
-    odd = randn(gen(9), 61, 411, dtype=dtype)      # rows on no 16 bytes
+    odd = randn(gen(9), M, 411, dtype=dtype)      # rows on no 16 bytes
     ys, base = odd[:, :136], before[:, :136]
     check_lora(xs, a, b, s, ids, base, run_lora(xs, a, b, s, ids, base, dtype, ys))
 
