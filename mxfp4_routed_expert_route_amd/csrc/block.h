@@ -73,7 +73,7 @@ struct LoraArgs {
   float* v;                 // inner sums, [lora_splits][M][R]
 };
 hipError_t launch_lora_add(const LoraArgs& a, bool f32, hipStream_t stream);
-// lora_tall.hip: sets *done, or leaves the call to others (fewer than `least` rows a tile, R > 64).
-hipError_t launch_lora_tall(const LoraArgs& a, bool f32, int wide, int least, hipStream_t stream, bool* done);
+// lora_tall.hip: sets *done, or leaves the call to others (few rows, R > 64).
+hipError_t launch_lora_tall(const LoraArgs& a, bool f32, int wide, hipStream_t stream, bool* done);
 
 }  // namespace moe

@@ -8,7 +8,6 @@
 #include "block_plan.h"
 #include "lds_copy.h"
 #include "lora_core.h"
-#include <cstdlib>
 
 namespace moe {
 namespace {
@@ -461,7 +460,6 @@ hipError_t launch_shrink(const LoraArgs& a, bool tall, hipStream_t stream, int* 
   // workgroups to fill the GPU, with four chunks of K or two a wavefront at least
   const int64_t fill = (tall ? 512 : 256) / (tiles * rank_blocks), most_splits = tall ? chunks / 4 : chunks / 16;
   int64_t s = fill < most_splits ? fill : most_splits;
-  if (getenv("LORA_SPLITS")) s = atoi(getenv("LORA_SPLITS"));
   if (s > lora_max_splits(a.M)) s = lora_max_splits(a.M);
   *splits = s < 1 ? 1 : static_cast<int>(s);
   const int per = rank_blocks * *splits;
@@ -484,8 +482,7 @@ hipError_t launch_expand(const LoraArgs& a, int wide, int splits, hipStream_t st
   const int64_t touched = a.M < a.L ? a.M : a.L;
   // a multiple of 8 for the XCDs; no more than are resident at once
   const int64_t pairs = (tile_bound(a.M, touched + 1, 16) * col_blocks + 7) / 8 * 8;
-  int64_t most = 256 * (KS <= 2 ? 4 : KS == 4 ? 3 : 2);
-  if (getenv("LORA_WG")) most = atoi(getenv("LORA_WG"));
+  const int64_t most = 256 * (KS <= 2 ? 4 : KS == 4 ? 3 : 2);
   expand_kernel<Out, KS><<<dim3(static_cast<unsigned>(pairs < most ? pairs : most)), dim3(256), 0, stream>>>(
       a, col_blocks, wide, splits);
   return hipGetLastError();
@@ -496,23 +493,19 @@ hipError_t launch_add(const LoraArgs& a, int wide, hipStream_t stream) {
   const int64_t touched = a.M < a.L ? a.M : a.L;
   const int col_blocks = (a.N + 255) / 256;
   const int64_t small = tile_bound(a.M, touched + 1, 16) * col_blocks;   // and the rows without an adapter
-  const char* e = getenv("LORA_SMALL");
-  if (a.R <= 64 && small <= (e ? atoi(e) : 256)) {
+  if (a.R <= 64 && small <= 256) {
     const dim3 grid(static_cast<unsigned>(small)), block(1024);
     if (a.R <= 16) small_kernel<Out, 1><<<grid, block, 0, stream>>>(a, col_blocks, wide);
     else if (a.R <= 32) small_kernel<Out, 2><<<grid, block, 0, stream>>>(a, col_blocks, wide);
     else small_kernel<Out, 4><<<grid, block, 0, stream>>>(a, col_blocks, wide);
     return hipGetLastError();
   }
-  {
-    bool done;
-    const hipError_t err = launch_lora_tall(a, sizeof(Out) == 4, wide, getenv("LORA_LEAST") ? atoi(getenv("LORA_LEAST")) : 24, stream, &done);
-    if (err != hipSuccess || done) return err;
-  }
-  bool tall = a.M > 16 * touched;   // more than 16 rows an adapter on average
-  if (getenv("LORA_TALL")) tall = atoi(getenv("LORA_TALL"));
+  bool done;
+  hipError_t err = launch_lora_tall(a, sizeof(Out) == 4, wide, stream, &done);
+  if (err != hipSuccess || done) return err;
+  const bool tall = a.M > 16 * touched;   // more than 16 rows an adapter on average
   int splits = 1;
-  const hipError_t err = a.R <= 16   ? launch_shrink<1>(a, tall, stream, &splits)
+  err = a.R <= 16   ? launch_shrink<1>(a, tall, stream, &splits)
                          : a.R <= 32 ? launch_shrink<2>(a, tall, stream, &splits)
                                      : launch_shrink<4>(a, tall, stream, &splits);
   if (err != hipSuccess) return err;

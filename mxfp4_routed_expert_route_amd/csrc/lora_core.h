@@ -122,6 +122,8 @@ __device__ __forceinline__ void split(const float (&v)[8], bf16x8 (&part)[kParts
 template <class Out>
 constexpr int kPartsOf = sizeof(Out) == 4 ? 3 : 2;
 
+typedef uint32_t Words __attribute__((ext_vector_type(4)));
+
 // kCols neighbouring columns of a row (4 or a multiple of 8), `left` of them within the matrix;
 // whole: all of them, on 16 bytes (4 bf16: on 8).
 template <class Out, int kCols>
@@ -141,8 +143,8 @@ struct Cols {
       } else {
 #pragma unroll
         for (int i = 0; i < kWords; i += 4) {
-          const uint4 d = *reinterpret_cast<const uint4*>(p + i * 4 / sizeof(Out));
-          w[i] = d.x; w[i + 1] = d.y; w[i + 2] = d.z; w[i + 3] = d.w;
+          const Words d = __builtin_nontemporal_load(reinterpret_cast<const Words*>(p + i * 4 / sizeof(Out)));
+          w[i] = d[0]; w[i + 1] = d[1]; w[i + 2] = d[2]; w[i + 3] = d[3];
         }
       }
     } else {
@@ -180,7 +182,8 @@ struct Cols {
       } else {
 #pragma unroll
         for (int i = 0; i < kWords; i += 4)
-          *reinterpret_cast<uint4*>(p + i * 4 / sizeof(Out)) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+          __builtin_nontemporal_store(Words{w[i], w[i + 1], w[i + 2], w[i + 3]},
+                                      reinterpret_cast<Words*>(p + i * 4 / sizeof(Out)));
       }
     } else {
 #pragma unroll
