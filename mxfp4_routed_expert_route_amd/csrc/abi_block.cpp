@@ -4,6 +4,7 @@
 
 #include "../../include/moe_block.h"
 #include "block.h"
+#include "block_plan.h"
 #include "validate_block.h"
 
 namespace {
@@ -50,8 +51,10 @@ moe_status moe_balance_loss(const void* logits, int32_t logits_type, int64_t T, 
   const moe_status s = moe::check_balance(logits, logits_type, T, E, k, score, topk_ids, seq_offsets, n_seqs,
                                           loss, counts, dloss, add_to, dlogits, ws, ws_bytes);
   if (s != MOE_OK) return s;
+  const size_t sums = (static_cast<size_t>(moe::balance_slots(T, n_seqs)) * sizeof(double) + 255) / 256 * 256;
   const moe::BalanceArgs a{logits, T, E, k, score == MOE_SCORE_SIGMOID, topk_ids, seq_offsets, n_seqs,
-                           loss, counts, dloss, add_to, dlogits, static_cast<double*>(ws)};
+                           loss, counts, dloss, add_to, dlogits, static_cast<double*>(ws),
+                           T == 0 ? nullptr : reinterpret_cast<int32_t*>(static_cast<char*>(ws) + sums)};
   return from_hip(moe::launch_balance(a, logits_type == MOE_BF16, as_stream(stream)));
 }
 
@@ -68,7 +71,7 @@ moe_status moe_balance_loss_grad(const void* logits, int32_t logits_type, int64_
                                                counts, dloss, add_to, dlogits);
   if (s != MOE_OK || T == 0) return s;
   const moe::BalanceArgs a{logits, T, E, k, score == MOE_SCORE_SIGMOID, nullptr, seq_offsets, n_seqs,
-                           nullptr, const_cast<int32_t*>(counts), dloss, add_to, dlogits, nullptr};
+                           nullptr, const_cast<int32_t*>(counts), dloss, add_to, dlogits, nullptr, nullptr};
   return from_hip(moe::launch_balance(a, logits_type == MOE_BF16, as_stream(stream)));
 }
 

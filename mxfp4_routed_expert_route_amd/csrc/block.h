@@ -51,6 +51,7 @@ struct BalanceArgs {
   const void* add;
   void* dlogits;            // nullptr: no gradient
   double* slots;            // sums over a chunk's tokens of a sequence, at [chunk + sequence]
+  int32_t* partial;         // counts of long sequences by chunk: block_plan.h
 };
 hipError_t launch_balance(const BalanceArgs& a, bool bf16, hipStream_t stream);
 

@@ -21,11 +21,16 @@ inline int64_t norm_grad_groups(int64_t rows, int H) {
   return rows < most ? rows : most;
 }
 
-// moe_balance_loss: tokens per workgroup.
-constexpr int kBalanceMinChunk = 8;
+// moe_balance_loss: tokens per workgroup at least, and the sums that the workgroups leave.
+constexpr int kBalanceMinChunk = 16;
 inline int64_t balance_slots(int64_t T, int n_seqs) {
   return (T + kBalanceMinChunk - 1) / kBalanceMinChunk + n_seqs;
 }
+// A sequence of more (token, slot) pairs is counted by a launch of its own, in chunks of at least
+// kCountChunk tokens, and has more than kLongTokens tokens: chunk c's counts of the sequence that
+// begins at token t are at slot c + t / kLongTokens, no two at one.
+constexpr int kShortPairs = 8192, kLongTokens = kShortPairs / kMaxK, kCountChunk = 256;
+inline int64_t balance_count_slots(int64_t T) { return T / kCountChunk + T / kLongTokens + 2; }
 
 // moe_lora_add: rows of partial inner sums, [splits of K][M], and the splits that fit them.
 constexpr int64_t kLoraPartialRows = 8192;

@@ -89,7 +89,8 @@ moe_status check_rms_norm_grad(const void* s, int64_t s_stride, int64_t rows, in
 moe_status balance_workspace(int64_t T, int32_t E, int32_t n_seqs, size_t* bytes) {
   if (T < 0 || E < 1 || n_seqs < 1) return MOE_ERR_INVALID_ARGUMENT;
   if (E > kMaxE || T > INT32_MAX || n_seqs > kMaxSequences) return MOE_ERR_UNSUPPORTED;
-  *bytes = align_up(static_cast<size_t>(balance_slots(T, n_seqs)) * sizeof(double), 256);
+  *bytes = align_up(static_cast<size_t>(balance_slots(T, n_seqs)) * sizeof(double), 256) +
+           align_up(static_cast<size_t>(balance_count_slots(T)) * static_cast<size_t>(E) * sizeof(int32_t), 256);
   return MOE_OK;
 }
 
