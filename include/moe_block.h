@@ -154,7 +154,8 @@ moe_status moe_lora_group(const int32_t* adapter, int64_t M, int32_t L, int32_t*
  *   offsets, rows    as written by moe_lora_group for these M rows and L adapters
  *   base     bf16 or fp32 [M][N], by y_type, base_stride between rows, or NULL; 16-byte aligned
  *   y        bf16 or fp32 [M][N], by y_type, y_stride between rows   out; 16-byte aligned; may be
- *            base's buffer if the strides agree (rows without an adapter are then not touched)
+ *            base's buffer if the strides agree (rows without an adapter are then not touched), and
+ *            overlaps nothing else
  *   ws       moe_lora_add_workspace_bytes(M, N, K, R, L) bytes, 16-byte aligned; contents on entry
  *            are ignored
  * K is a positive multiple of 8, at most 65536; R a positive multiple of 8, at most 256 (an adapter of

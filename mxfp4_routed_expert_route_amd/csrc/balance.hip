@@ -80,11 +80,27 @@ __global__ __launch_bounds__(256) void zero_kernel(int32_t* p, int64_t n) {
   for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) p[i] = 0;
 }
 
-// Adds the experts of pairs i0 .. i1 - 1 to `bins` in LDS.
+// Counts the experts of pairs i0 .. i1 - 1 in `bins` in LDS, by the whole workgroup; they are there
+// after the caller's next barrier.  Eight ids a thread are on their way at once.
 __device__ __forceinline__ void count_pairs(const int32_t* ids, int64_t i0, int64_t i1, int E, int* bins) {
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += blockDim.x) {
-    const int e = ids[i];
-    if (static_cast<unsigned>(e) < static_cast<unsigned>(E)) atomicAdd(&bins[e], 1);
+  const int n = blockDim.x;
+  int e[8];
+  auto load = [&](int64_t i) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t at = i + static_cast<int64_t>(u) * n;
+      const int id = ids[at < i1 ? at : i1 - 1];
+      e[u] = at < i1 ? id : -1;
+    }
+  };
+  load(i0 + threadIdx.x);
+  for (int b = threadIdx.x; b < E; b += n) bins[b] = 0;
+  __syncthreads();
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += 8 * n) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (static_cast<unsigned>(e[u]) < static_cast<unsigned>(E)) atomicAdd(&bins[e[u]], 1);
+    if (i + 8 * n < i1) load(i + 8 * n);
   }
 }
 
@@ -97,8 +113,6 @@ __global__ __launch_bounds__(1024) void count_kernel(BalanceArgs a, int chunk) {
   while (t < t1) {   // uniform over the workgroup
     const Segment g = segment_at(q, t, t1);
     if (g.s < a.n_seqs && g.n * a.k > kShortPairs) {
-      for (int e = threadIdx.x; e < a.E; e += 1024) bins[e] = 0;
-      __syncthreads();
       count_pairs(a.ids, t * a.k, g.end * a.k, a.E, bins);
       __syncthreads();
       int32_t* to = a.partial + (blockIdx.x + g.begin / kLongTokens) * a.E;
@@ -218,8 +232,6 @@ __global__ __launch_bounds__(256) void balance_kernel(BalanceArgs a, int chunk, 
     const int32_t* counts = a.counts + static_cast<int64_t>(g.s) * E;
     if (a.ids != nullptr) {
       if (g.n * a.k <= kShortPairs) {
-        for (int e = threadIdx.x; e < E; e += 256) bins[e] = 0;
-        __syncthreads();
         count_pairs(a.ids, g.begin * a.k, (g.begin + g.n) * a.k, E, bins);
       } else {
         const int64_t first = g.begin / count_chunk, last = (g.begin + g.n - 1) / count_chunk;

@@ -28,13 +28,21 @@ __device__ __forceinline__ void inner_products(const uint16_t* x, const uint16_t
   };
   auto load = [&](Chunk& d, int c) {
     const int k0 = 64 * c + 8 * g;
-    const bool whole = 64 * c + 64 <= K;   // uniform; zeros past K
+    if (64 * c + 64 <= K) {   // uniform
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool here = whole || k0 + 32 * h < K;
+      for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int f = 0; f < NF; ++f) d.w[f][h] = load_bf16x8(w[f] + k0 + 32 * h, here);
-      d.x[h] = load_bf16x8(x + k0 + 32 * h, here);
+        for (int f = 0; f < NF; ++f) d.w[f][h] = load_bf16x8(w[f] + k0 + 32 * h, true);
+        d.x[h] = load_bf16x8(x + k0 + 32 * h, true);
+      }
+    } else {   // zeros past K
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool here = k0 + 32 * h < K;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) d.w[f][h] = load_bf16x8(w[f] + k0 + 32 * h, here);
+        d.x[h] = load_bf16x8(x + k0 + 32 * h, here);
+      }
     }
   };
   Chunk ring[kDepth];
@@ -389,6 +397,9 @@ __global__ __launch_bounds__(1024) void small_kernel(LoraArgs a, int col_blocks,
   const int r16 = lane & 15, g = lane >> 4;
   const int tile_no = blockIdx.x / col_blocks;
   const int n0 = (blockIdx.x - tile_no * col_blocks) * 256 + 16 * wave;
+  // up to 64 rows: their numbers come with the offsets, not after them
+  const bool few = a.M <= 64;   // uniform
+  const int first_rows = few ? a.rows[lane < a.M ? lane : 0] : 0;
   const Tiles<16> tiles(a.offsets, a.L, static_cast<int>(a.M));
   if (tile_no >= tiles.total) return;   // uniform over the workgroup
   const Tile tile = tiles.find(tile_no);
@@ -398,7 +409,8 @@ __global__ __launch_bounds__(1024) void small_kernel(LoraArgs a, int col_blocks,
   Out* y = static_cast<Out*>(a.y);
   const int c0 = n0 + 4 * g, left = a.N - c0;
   const bool whole = wide && left >= 4;
-  const int row = a.rows[tile.begin + (r16 < tile.rows ? r16 : 0)];
+  const int p = tile.begin + (r16 < tile.rows ? r16 : 0);
+  const int row = few ? __shfl(first_rows, p, 64) : a.rows[p];
   const bool live = r16 < tile.rows && static_cast<unsigned>(row) < static_cast<unsigned>(a.M);
   const bool out = live && left > 0;
   Cols<Out, 4> cols;

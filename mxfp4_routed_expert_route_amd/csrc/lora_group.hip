@@ -28,7 +28,8 @@ __global__ __launch_bounds__(64 * W) void group_kernel(const int32_t* __restrict
     const int id = adapter[i];
     return static_cast<unsigned>(id) < static_cast<unsigned>(L) ? id : L;
   };
-  for (int64_t i = begin + lane; i < end; i += 64) atomicAdd(&mine[bin_of(i)], 1);
+  const int first_bin = begin + lane < end ? bin_of(begin + lane) : -1;   // of the first 64 rows
+  for (int64_t i = begin + lane; i < end; i += 64) atomicAdd(&mine[i < begin + 64 ? first_bin : bin_of(i)], 1);
   __syncthreads();
   // exclusive sums over (bin, wavefront), 64 W bins at a time
   for (int b0 = 0; b0 < bins; b0 += 64 * W) {
@@ -61,7 +62,7 @@ __global__ __launch_bounds__(64 * W) void group_kernel(const int32_t* __restrict
   for (int64_t i0 = begin; i0 < end; i0 += 64) {   // uniform per wavefront
     const int64_t i = i0 + lane;
     const bool here = i < end;
-    const int bin = here ? bin_of(i) : -1;
+    const int bin = i0 == begin ? first_bin : here ? bin_of(i) : -1;
     uint64_t same = __builtin_amdgcn_ballot_w64(here);
 #pragma unroll
     for (int bit = 0; bit < 11; ++bit) {   // bins number at most 1025

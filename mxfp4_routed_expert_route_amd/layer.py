@@ -121,6 +121,57 @@ def run_layer_fp8(dev: dict, b: LayerBuffers, limit: float, stream=None, **scori
     binding.moe_combine(b.y_sorted, b.topk_weights, b.scatter, b.y, stream)
 
 
+@dataclasses.dataclass
+class BlockBuffers:
+    """Buffers of run_block_fp8: the layer's, the norm's outputs, the router's logits, the shared
+    projection's result, and the batch's rows by adapter (L = 0: no adapters)."""
+    layer: LayerBuffers
+    sum: torch.Tensor
+    h: torch.Tensor
+    hq: torch.Tensor
+    hs: torch.Tensor
+    logits: torch.Tensor
+    shared: torch.Tensor
+    adapter_offsets: torch.Tensor
+    adapter_rows: torch.Tensor
+    lora_ws: torch.Tensor
+
+    @classmethod
+    def allocate_fp8(cls, T, E, k, H, I, N, L=0, R=8, device="cuda"):
+        dev = torch.device(device)
+
+        def new(*shape, dtype=torch.bfloat16):
+            return torch.empty(shape, dtype=dtype, device=dev)
+
+        ws = max(binding.moe_lora_add_workspace_bytes(T, n, H, R, L) for n in (E, N)) if L else 0
+        return cls(LayerBuffers.allocate_fp8(T, E, k, H, I, device), sum=new(T, H), h=new(T, H),
+                   hq=new(T, H, dtype=torch.float8_e4m3fn), hs=new(T, (H + 127) // 128, dtype=torch.float32),
+                   logits=new(T, E, dtype=torch.float32), shared=new(T, N),
+                   adapter_offsets=new(L + 1, dtype=torch.int32), adapter_rows=new(T, dtype=torch.int32),
+                   lora_ws=new(ws, dtype=torch.uint8))
+
+
+def run_block_fp8(dev: dict, b: BlockBuffers, limit: float, eps: float = 1e-6, stream=None, **scoring):
+    """The layer with what stands around it: residual addition and norm (bf16 for the experts, FP8 for
+    the dense products), the router's product and a shared projection beside the experts, each with
+    the requests' adapters if dev["adapter"] is given, then run_layer_fp8 on the routed rows.
+
+    dev: x, residual [T, H], norm [H], router [E, H] and shared [N, H] in block-scaled FP8 with
+    router_s and shared_s, w1, w1_s, w2, w2_s; with adapters adapter [T], scaling [L] or None, and
+    router_a, router_b, shared_a, shared_b.  Leaves the stream in b.sum, the experts' sum in
+    b.layer.y and the projection in b.shared."""
+    binding.moe_rms_norm(dev["x"], dev["norm"], eps, residual=dev["residual"], sum=b.sum, y=b.h, q=b.hq,
+                         scale=b.hs, stream=stream)
+    binding.moe_gemm_fp8(b.hq, b.hs, dev["router"], dev["router_s"], b.logits, stream=stream)
+    binding.moe_gemm_fp8(b.hq, b.hs, dev["shared"], dev["shared_s"], b.shared, stream=stream)
+    if dev.get("adapter") is not None:
+        binding.moe_lora_group(dev["adapter"], dev["router_a"].shape[0], b.adapter_offsets, b.adapter_rows, stream)
+        for name, y in (("router", b.logits), ("shared", b.shared)):
+            binding.moe_lora_add(b.h, dev[name + "_a"], dev[name + "_b"], dev.get("scaling"), b.adapter_offsets,
+                                 b.adapter_rows, y, y, b.lora_ws, stream)
+    run_layer_fp8(dict(dev, x=b.h, logits=b.logits), b.layer, limit, stream, **scoring)
+
+
 def bf16_tensor_to_f32(t: torch.Tensor) -> np.ndarray:
     """Exact bf16 -> fp32 on the host (for comparisons)."""
     return t.float().cpu().numpy()

@@ -130,7 +130,7 @@ def test_norm_outputs_do_not_depend_on_one_another(rows, H):
                 assert torch.equal(one[n].view(torch.uint8), both[n].view(torch.uint8)), n
 
 
-@pytest.mark.parametrize("H", [400, 4096])
+@pytest.mark.parametrize("H", [64, 208, 400, 4096])
 def test_norm_of_rows_at_every_magnitude(H):
     g = gen(6)
     x = torch.randn(40, H, generator=g)
@@ -284,20 +284,21 @@ def test_norm_grad_in_place_and_of_a_slice():
         assert torch.equal(t, dx) and torch.equal(out, dw)
 
 
-def test_norm_grad_of_extreme_rows():
+@pytest.mark.parametrize("H", [64, 256, 512, 4096])
+def test_norm_grad_of_extreme_rows(H):
     g = gen(13)
-    s = torch.randn(12, 512, generator=g)
+    s = torch.randn(12, H, generator=g)
     for i in range(12):
         s[i] *= 2.0 ** (-120 + 20 * i)
     s = s.bfloat16().to(DEV)
     # dy beside it, so that dx stays within bf16
-    dy = randn(g, 12, 512)
+    dy = randn(g, 12, H)
     for i in range(12):
         dy[i] *= 2.0 ** min(0, -60 + 20 * i)
-    w = randn(g, 512)
+    w = randn(g, H)
     dx, dw = norm_grad(s, w, 0.0, dy)
     check_norm_grad(s, w, 0.0, dy, None, dx, dw)
-    z = torch.zeros(4, 512, dtype=torch.bfloat16, device=DEV)       # zero rows: dx = dy w / sqrt(eps)
+    z = torch.zeros(4, H, dtype=torch.bfloat16, device=DEV)       # zero rows: dx = dy w / sqrt(eps)
     dx, dw = norm_grad(z, w, 1e-6, dy[4:8].contiguous())
     check_norm_grad(z, w, 1e-6, dy[4:8].contiguous(), None, dx, dw)
     assert not dw.any()
@@ -544,7 +545,9 @@ def check_lora(x, a, b, s, ids, base, y):
 
 LORA = [(1, 1, 8, 8, 1), (1, 64, 64, 16, 3), (2, 17, 24, 8, 2), (16, 256, 128, 16, 1), (17, 257, 136, 24, 4), (33, 1003, 264, 8, 5),
         (40, 48, 2064, 40, 3), (100, 520, 512, 64, 6), (70, 96, 1024, 72, 2), (50, 272, 256, 128, 3), (37, 80, 192, 136, 2),
-        (65, 304, 320, 256, 2), (300, 512, 4096, 16, 64), (200, 64, 72, 32, 70), (1, 4096, 4096, 16, 8), (3, 96, 65536, 8, 2)]
+        (65, 304, 320, 256, 2), (300, 512, 4096, 16, 64), (200, 64, 72, 32, 70), (1, 4096, 4096, 16, 8), (3, 96, 65536, 8, 2),
+        (1500, 600, 200, 16, 4), (1500, 600, 136, 32, 4), (1500, 530, 1032, 64, 3), (1300, 1000, 72, 8, 2), (600, 2048, 64, 16, 40),
+        (2100, 2049, 128, 200, 5), (900, 4096, 64, 24, 300)]
 
 
 @pytest.mark.parametrize("M,N,K,R,L", LORA)
@@ -641,6 +644,99 @@ def test_lora_without_rows():
     offsets, rows = group(np.empty(0, int), 2)
     binding.moe_lora_add(e, a, b, None, offsets, rows, None, e.clone(), None)
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- together
+
+def _block(seed, T=90, E=32, k=4, H=512, I=256, N=384, L=3, R=16):
+    """Inputs of layer.run_block_fp8 and their float64 values."""
+    r = np.random.default_rng(seed)
+    g = gen(seed)
+
+    def fp8(n, K, lead=()):
+        q = torch.from_numpy(quantize_fp8(r.normal(size=(int(np.prod(lead, dtype=int)) * n, K)))[0]).view(*lead, n, K)
+        s = (r.random((*lead, -(-n // 128), -(-K // 128))) + 0.5) * 400.0 / 448.0 / 100.0 / K ** 0.5
+        return q.to(DEV), torch.from_numpy(s.astype(np.float32)).to(DEV)
+
+    dev = dict(x=randn(g, T, H), residual=randn(g, T, H), norm=(1 + 0.2 * torch.randn(H, generator=g)).to(DEV))
+    for name, n in (("router", E), ("shared", N)):
+        dev[name], dev[name + "_s"] = fp8(n, H)
+        dev[name + "_a"], dev[name + "_b"] = randn(g, L, R, H, scale=H ** -0.5), randn(g, L, n, R, scale=R ** -0.5)
+    dev["w1"], dev["w1_s"] = fp8(2 * I, H, (E,))
+    dev["w2"], dev["w2_s"] = fp8(H, I, (E,))
+    dev["adapter"] = torch.from_numpy(r.integers(-1, L, size=T).astype(np.int32)).to(DEV)
+    dev["scaling"] = torch.from_numpy((r.random(L) + 0.5).astype(np.float32)).to(DEV)
+    return dev, (T, E, k, H, I, N, L, R)
+
+
+def test_block_runs_its_parts_together():
+    """norm -> FP8 router and projection, each with adapters -> routed experts, against the parts' oracles."""
+    from mxfp4_routed_expert_route_amd import layer
+    from oracle.fp8 import gemm_fp8, route_scored
+    dev, (T, E, k, H, I, N, L, R) = _block(3)
+    b = layer.BlockBuffers.allocate_fp8(T, E, k, H, I, N, L, R)
+    how = dict(score="sigmoid", scale=1.5)
+    layer.run_block_fp8(dev, b, 10.0, **how)
+    torch.cuda.synchronize()
+    check_norm(dev["x"], dev["norm"], 1e-6, dev["residual"], dict(sum=b.sum, y=b.h, q=b.hq, scale=b.hs))
+    ids = dev["adapter"].cpu().numpy()
+    for name, y in (("router", b.logits), ("shared", b.shared)):
+        base, _ = gemm_fp8(b.hq.view(torch.uint8).cpu().numpy(), f64(b.hs), dev[name].cpu().numpy(), f64(dev[name + "_s"]))
+        want = block.lora_add(f64(b.h), f64(dev[name + "_a"]), f64(dev[name + "_b"]), f64(dev["scaling"]), ids, base)[0]
+        # bf16: the product rounds once, its adapters' sum again, of the rounded value
+        tol = 4 * HALF if y.dtype == torch.bfloat16 else 2.0 ** -14
+        assert np.abs(f64(y) - want).max() <= tol * np.abs(want).max()
+    want = route_scored(f64(b.logits), k, score="sigmoid", scale=1.5)
+    assert np.array_equal(b.layer.topk_ids.cpu().numpy(), want[0])
+    alone = layer.LayerBuffers.allocate_fp8(T, E, k, H, I)
+    layer.run_layer_fp8(dict(dev, x=b.h, logits=b.logits), alone, 10.0, **how)
+    assert torch.equal(alone.y, b.layer.y) and b.layer.y.isfinite().all() and b.layer.y.any()
+    # the next block's stream takes this one's result; without adapters the call is the dense products alone
+    dev2 = dict(dev, x=b.layer.y, residual=b.sum, adapter=None)
+    b2 = layer.BlockBuffers.allocate_fp8(T, E, k, H, I, N)
+    layer.run_block_fp8(dev2, b2, 10.0, **how)
+    y = torch.empty_like(b2.shared)
+    binding.moe_gemm_fp8(b2.hq, b2.hs, dev["shared"], dev["shared_s"], y)
+    assert torch.equal(y, b2.shared) and b2.layer.y.isfinite().all()
+
+
+def test_router_training_step_against_differences():
+    """The balance loss's gradient through the router's product and the norm, against differences of the
+    loss in 64 bits."""
+    T, H, E, k, eps = 48, 64, 12, 2, 1e-5
+    g = gen(17)
+    x, w, router = randn(g, T, H), (1 + 0.2 * torch.randn(H, generator=g)).to(DEV), randn(g, E, H, scale=0.2)
+    cuts = torch.tensor([0, 20, 45], dtype=torch.int32, device=DEV)
+    dloss = torch.tensor([0.7, 1.3], device=DEV)
+    h = torch.empty_like(x)
+    binding.moe_rms_norm(x, w, eps, y=h)
+    logits = (h.float() @ router.float().t()).contiguous()
+    ids, weights = torch.empty(T, k, dtype=torch.int32, device=DEV), torch.empty(T, k, device=DEV)
+    binding.moe_route_scored(logits, k, ids, weights)
+    loss, counts = torch.empty(2, device=DEV), torch.empty(2, E, dtype=torch.int32, device=DEV)
+    ws = torch.empty(binding.moe_balance_loss_workspace_bytes(T, E, 2), dtype=torch.uint8, device=DEV)
+    dlogits = torch.empty_like(logits)
+    binding.moe_balance_loss(logits, ids, loss, counts, ws, seq_offsets=cuts, dloss=dloss, dlogits=dlogits)
+    scale = 2.0 ** 10      # dh in bf16, far from its smallest values
+    dh = (dlogits @ router.float() * scale).bfloat16()
+    dx, dw = torch.empty_like(x), torch.empty(H, device=DEV)
+    nws = torch.empty(binding.moe_rms_norm_grad_workspace_bytes(T, H), dtype=torch.uint8, device=DEV)
+    binding.moe_rms_norm_grad(x, w, eps, dh, dx, dw, nws)
+
+    X, W, Q, I, C = f64(x), f64(w), f64(router), ids.cpu().numpy(), cuts.cpu().tolist()
+
+    def total(X, W):
+        return (block.balance_loss(block.rms_norm(X, None, W, eps)[1] @ Q.T, I, "softmax", C)[0] * f64(dloss)).sum()
+
+    r = np.random.default_rng(1)
+    for _ in range(6):      # along random directions of x and of the weight
+        u, v = r.normal(size=X.shape), r.normal(size=W.shape)
+        d = 1e-5
+        by_x = (total(X + d * u, W) - total(X - d * u, W)) / (2 * d) * scale
+        by_w = (total(X, W + d * v) - total(X, W - d * v)) / (2 * d) * scale
+        # h, dh and dx are rounded to bf16: three half steps of each term, and as much for h in the logits
+        assert abs((f64(dx) * u).sum() - by_x) <= 6 * HALF * np.abs(f64(dx) * u).sum()
+        assert abs((f64(dw) * v).sum() - by_w) <= 6 * HALF * np.abs(f64(dw) * v).sum()
 
 
 # ---------------------------------------------------------------- streams and graphs
