@@ -99,7 +99,8 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_grad_kernel(NormGrad
       v = row_sum<kLanes>(both(r, row, f), sums[2]);
       if constexpr (kLanes == 0) __syncthreads();   // sums[2] may be next in line too
     }
-    const float rstd = row_rstd(v.x, a.H, a.eps, f);
+    // a row that is not there adds zeros (its zeros with an eps of 0 would be NaN)
+    const float rstd = row < a.rows ? row_rstd(v.x, a.H, a.eps, f) : 0.f;
     const float c = rstd * v.y / static_cast<float>(a.H);   // mean(z u)
 #pragma unroll
     for (int i = 0; i < C; ++i) {
