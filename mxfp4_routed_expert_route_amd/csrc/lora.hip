@@ -109,10 +109,9 @@ __global__ __launch_bounds__(512) void shrink_kernel(LoraArgs a, int tile0, int 
 // themselves, in whole lines (8 rows x 128 bytes a copy), four chunks of K deep; a wavefront takes 16
 // of the rows.  Piece c (16 bytes) of LDS row r sits at place c ^ ((r >> 1) & 7), so that operand
 // reads meet no bank conflict.
-template <int NF>
 __global__ __launch_bounds__(256) void shrink_stream_kernel(LoraArgs a, int tile0, int rank_blocks, int splits) {
-  constexpr int kRows = 64, kLines = kRows + 16 * NF, kStages = 4, W = 4;
-  constexpr int kAll = kLines / 8, kEach = (kAll + W - 1) / W, kUneven = kAll % W;   // copies of a chunk
+  constexpr int NF = 4, kRows = 64, kLines = kRows + 16 * NF, kStages = 4, W = 4;
+  constexpr int kEach = kLines / 8 / W;   // copies of a chunk
   __shared__ __attribute__((aligned(16))) unsigned char lds[kStages][kLines * 128];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -142,7 +141,6 @@ __global__ __launch_bounds__(256) void shrink_stream_kernel(LoraArgs a, int tile
       from[i] = a.a + (static_cast<int64_t>(tile.adapter) * a.R + (rank < a.R ? rank : 0)) * K;
     }
   }
-  const bool fewer = kUneven != 0 && wave >= kUneven;   // one copy less
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) unsigned char*)&lds[0][0]));
   auto copy = [&](int c) {
@@ -150,8 +148,7 @@ __global__ __launch_bounds__(256) void shrink_stream_kernel(LoraArgs a, int tile
     const int k = at < K ? at : 0;   // past K: any, the operands are zeroed
 #pragma unroll
     for (int i = 0; i < kEach; ++i)
-      if (i + 1 < kEach || !fewer)   // uniform
-        copy16_global(from[i] + k, lds0 + (c - begin) % kStages * (kLines * 128) + 1024 * (wave + W * i));
+      copy16_global(from[i] + k, lds0 + (c - begin) % kStages * (kLines * 128) + 1024 * (wave + W * i));
   };
   floatx4 acc[NF];
 #pragma unroll
@@ -161,14 +158,10 @@ __global__ __launch_bounds__(256) void shrink_stream_kernel(LoraArgs a, int tile
     if (begin + s < end) copy(begin + s);
   const int place = r16 * 128 + 16 * (g ^ ((r16 >> 1) & 7));   // piece g; piece g + 4 is at ^ 64
   for (int c = begin; c < end; ++c) {
-    if (c + kStages - 1 < end) {   // uniform: this chunk's copies are the oldest
-      if (fewer)
-        wait_copies<(kStages - 2) * (kEach - 1)>();
-      else
-        wait_copies<(kStages - 2) * kEach>();
-    } else {
+    if (c + kStages - 1 < end)   // uniform: this chunk's copies are the oldest
+      wait_copies<(kStages - 2) * kEach>();
+    else
       wait_copies<0>();
-    }
     wait_lds();
     barrier();   // all wavefronts' copies of it are there, and the chunk before it has been read
     if (c + kStages - 1 < end) copy(c + kStages - 1);
@@ -465,12 +458,16 @@ __global__ __launch_bounds__(1024) void small_kernel(LoraArgs a, int col_blocks,
 int64_t tile_bound(int64_t M, int64_t groups, int64_t rows) { return (M + (rows - 1) * groups) / rows; }
 
 template <int NF>
-hipError_t launch_shrink(const LoraArgs& a, bool tall, hipStream_t stream, int* splits) {
+hipError_t launch_shrink(const LoraArgs& a, hipStream_t stream, int* splits) {
   const int64_t touched = a.M < a.L ? a.M : a.L;
-  const int64_t tiles = tile_bound(a.M, touched, tall ? 64 : 16);
   const int rank_blocks = (a.R + 16 * NF - 1) / (16 * NF), chunks = (a.K + 63) / 64;
+  // Tiles of 64 rows need some fifty of them to fill the GPU without more splits of K than the second product
+  // reads at ease.  16 rows / 64 rows, us, 4096x4096 with 8 adapters: rank 128 2048 rows 46 / 61, 3000 69 / 59,
+  // 4096 78 / 71, 8191 142 / 106; rank 256 2048 rows 81 / 96.
+  const bool stream_rows = NF == 4 && rank_blocks > 1 && tile_bound(a.M, touched, 64) >= 48;
+  const int64_t tiles = tile_bound(a.M, touched, stream_rows ? 64 : 16);
   // workgroups to fill the GPU, with four chunks of K or two a wavefront at least
-  const int64_t fill = (tall ? 512 : 256) / (tiles * rank_blocks), most_splits = tall ? chunks / 4 : chunks / 16;
+  const int64_t fill = (stream_rows ? 512 : 256) / (tiles * rank_blocks), most_splits = chunks / (stream_rows ? 4 : 16);
   int64_t s = fill < most_splits ? fill : most_splits;
   if (s > lora_max_splits(a.M)) s = lora_max_splits(a.M);
   *splits = s < 1 ? 1 : static_cast<int>(s);
@@ -478,8 +475,8 @@ hipError_t launch_shrink(const LoraArgs& a, bool tall, hipStream_t stream, int* 
   const int64_t most = kMaxThreads / 512 / per;
   for (int64_t at = 0; at < tiles; at += most) {
     const dim3 grid(static_cast<unsigned>((tiles - at < most ? tiles - at : most) * per));
-    if (tall)
-      shrink_stream_kernel<NF><<<grid, dim3(256), 0, stream>>>(a, static_cast<int>(at), rank_blocks, *splits);
+    if (stream_rows)
+      shrink_stream_kernel<<<grid, dim3(256), 0, stream>>>(a, static_cast<int>(at), rank_blocks, *splits);
     else
       shrink_kernel<NF><<<grid, dim3(512), 0, stream>>>(a, static_cast<int>(at), rank_blocks, *splits);
     const hipError_t err = hipGetLastError();
@@ -505,21 +502,25 @@ hipError_t launch_add(const LoraArgs& a, int wide, hipStream_t stream) {
   const int64_t touched = a.M < a.L ? a.M : a.L;
   const int col_blocks = (a.N + 255) / 256;
   const int64_t small = tile_bound(a.M, touched + 1, 16) * col_blocks;   // and the rows without an adapter
-  if (a.R <= 64 && small <= 256) {
+  const int nf = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;   // fragments of 16 ranks
+  // One launch where no compute unit gets a second workgroup and each one's repeat of the first product
+  // is short.  One / two launches, us: 1x4096x4096 rank 8 6.5 / 9.5, 16 7.7 / 9.1, 32 11.3 / 9.4, 64 19.8 / 12.9;
+  // 77x1003x2064 rank 32 8.9 / 10.2, 64 13.4 / 12.5; 4x256x1024 rank 64 8.6 / 11.0; 64 adapters' 64 rows of
+  // 4096x4096 (1024 workgroups) rank 16 24 / 10.6.
+  if (a.R <= 64 && small <= 256 && static_cast<int64_t>(16 * nf) * a.K <= 98304) {
     const dim3 grid(static_cast<unsigned>(small)), block(1024);
-    if (a.R <= 16) small_kernel<Out, 1><<<grid, block, 0, stream>>>(a, col_blocks, wide);
-    else if (a.R <= 32) small_kernel<Out, 2><<<grid, block, 0, stream>>>(a, col_blocks, wide);
+    if (nf == 1) small_kernel<Out, 1><<<grid, block, 0, stream>>>(a, col_blocks, wide);
+    else if (nf == 2) small_kernel<Out, 2><<<grid, block, 0, stream>>>(a, col_blocks, wide);
     else small_kernel<Out, 4><<<grid, block, 0, stream>>>(a, col_blocks, wide);
     return hipGetLastError();
   }
   bool done;
   hipError_t err = launch_lora_tall(a, sizeof(Out) == 4, wide, stream, &done);
   if (err != hipSuccess || done) return err;
-  const bool tall = a.M > 16 * touched;   // more than 16 rows an adapter on average
   int splits = 1;
-  err = a.R <= 16   ? launch_shrink<1>(a, tall, stream, &splits)
-                         : a.R <= 32 ? launch_shrink<2>(a, tall, stream, &splits)
-                                     : launch_shrink<4>(a, tall, stream, &splits);
+  err = nf == 1   ? launch_shrink<1>(a, stream, &splits)
+        : nf == 2 ? launch_shrink<2>(a, stream, &splits)
+                  : launch_shrink<4>(a, stream, &splits);
   if (err != hipSuccess) return err;
   if (a.R <= 32) return launch_expand<Out, 1>(a, wide, splits, stream);
   if (a.R <= 64) return launch_expand<Out, 2>(a, wide, splits, stream);

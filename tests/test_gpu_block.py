@@ -547,7 +547,7 @@ LORA = [(1, 1, 8, 8, 1), (1, 64, 64, 16, 3), (2, 17, 24, 8, 2), (16, 256, 128, 1
         (40, 48, 2064, 40, 3), (100, 520, 512, 64, 6), (70, 96, 1024, 72, 2), (50, 272, 256, 128, 3), (37, 80, 192, 136, 2),
         (65, 304, 320, 256, 2), (300, 512, 4096, 16, 64), (200, 64, 72, 32, 70), (1, 4096, 4096, 16, 8), (3, 96, 65536, 8, 2),
         (1500, 600, 200, 16, 4), (1500, 600, 136, 32, 4), (1500, 530, 1032, 64, 3), (1300, 1000, 72, 8, 2), (600, 2048, 64, 16, 40),
-        (2100, 2049, 128, 200, 5), (900, 4096, 64, 24, 300)]
+        (2100, 2049, 128, 200, 5), (900, 4096, 64, 24, 300), (10, 300, 4096, 64, 2), (5, 70, 2064, 40, 2)]
 
 
 @pytest.mark.parametrize("M,N,K,R,L", LORA)
@@ -560,7 +560,8 @@ def test_lora_add(M, N, K, R, L, dtype):
 
 
 @pytest.mark.parametrize("M,N,K,R,L", [(6500, 72, 64, 16, 1), (7000, 100, 72, 40, 3), (8191, 64, 136, 64, 8), (6300, 130, 1032, 24, 2),
-                                       (20000, 65, 64, 8, 5), (9000, 33, 8, 64, 9), (7777, 264, 520, 32, 4), (40000, 16, 64, 48, 200)])
+                                       (20000, 65, 64, 8, 5), (9000, 33, 8, 64, 9), (7777, 264, 520, 32, 4), (40000, 16, 64, 48, 200),
+                                       (3300, 96, 200, 72, 2), (5000, 80, 1032, 256, 3), (4000, 70, 2064, 128, 40)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("packed", [False, True])
 def test_lora_add_many_rows(M, N, K, R, L, dtype, packed):
