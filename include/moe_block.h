@@ -132,7 +132,8 @@ moe_status moe_balance_loss_grad(const void* logits, int32_t logits_type, int64_
  *   offsets  int32 [L+1]    out; adapter a's rows are rows[offsets[a]] .. rows[offsets[a+1] - 1]
  *   rows     int32 [M]      out; row indices, ascending within an adapter; the rows without an
  *                           adapter, ascending, are behind offsets[L]
- * 1 <= L <= 1024.  M = 0 writes zeros to offsets.  One call serves every moe_lora_add of the batch.
+ * 1 <= L <= 1024; no two of the three overlap.  M = 0 writes zeros to offsets.  One call serves
+ * every moe_lora_add of the batch.
  */
 moe_status moe_lora_group(const int32_t* adapter, int64_t M, int32_t L, int32_t* offsets,
                           int32_t* rows, void* stream);

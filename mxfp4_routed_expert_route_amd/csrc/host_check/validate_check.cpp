@@ -211,7 +211,12 @@ int main() {
   expect("balance largest int64 T", balance(INT64_MAX, kMaxE, 1, 1), MOE_ERR_UNSUPPORTED);
   expect("balance sequences", balance(1, 2, 1, INT32_MAX), MOE_ERR_UNSUPPORTED);
   expect("balance ws", balance_workspace(INT32_MAX, kMaxE, kMaxSequences, &bytes), MOE_OK);
-  expect("lora group ok", check_lora_group(p, INT32_MAX, kMaxAdapters, p, p), MOE_OK);
+  auto at = [](uintptr_t v) { return reinterpret_cast<const void*>(v); };
+  const uintptr_t far = uintptr_t{1} << 40;
+  expect("lora group ok", check_lora_group(at(far), INT32_MAX, kMaxAdapters, at(2 * far), at(3 * far)), MOE_OK);
+  expect("lora group last row shared", check_lora_group(at(far), INT32_MAX, 2, at(far + (uintptr_t{1} << 33) - 8), at(3 * far)), MOE_ERR_INVALID_ARGUMENT);
+  expect("lora group beside", check_lora_group(at(far), INT32_MAX, 2, at(far + (uintptr_t{1} << 33) - 4), at(3 * far)), MOE_OK);
+  expect("lora group in place", check_lora_group(at(far), 4, 2, at(2 * far), at(far)), MOE_ERR_INVALID_ARGUMENT);
   auto lora = [&](int64_t M, int32_t N, int32_t K, int32_t R, int32_t L) {
     return check_lora_add(p, K, M, K, N, R, L, p, p, p, p, p, MOE_BF16, p, N, p, N, p, SIZE_MAX);
   };

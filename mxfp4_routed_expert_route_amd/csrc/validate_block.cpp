@@ -11,6 +11,12 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
+// Whether m and n 4-byte elements share any.
+bool overlap(const void* a, int64_t m, const void* b, int64_t n) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(a), q = reinterpret_cast<uintptr_t>(b);
+  return p < q ? q - p < static_cast<uintptr_t>(m) * 4 : p - q < static_cast<uintptr_t>(n) * 4;
+}
+
 moe_status check_rows(int64_t rows, int32_t H, int32_t multiple) {
   if (rows < 0 || H < 1) return MOE_ERR_INVALID_ARGUMENT;
   if (H % multiple != 0 || H > kMaxDim || rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
@@ -139,6 +145,9 @@ moe_status check_lora_group(const void* adapter, int64_t M, int32_t L, const voi
   if (M == 0) return MOE_OK;
   if (!adapter || !rows) return MOE_ERR_INVALID_ARGUMENT;
   if (!aligned(adapter, 4) || !aligned(rows, 4)) return MOE_ERR_MISALIGNED;
+  // rows are dealt out by counts of adapter: it has to stay as it was
+  if (overlap(adapter, M, rows, M) || overlap(adapter, M, offsets, L + 1) || overlap(rows, M, offsets, L + 1))
+    return MOE_ERR_INVALID_ARGUMENT;
   return MOE_OK;
 }
 

@@ -130,6 +130,9 @@ def test_lora_refusals(lib):
     assert lib.moe_lora_group(P, 4, 4, None, P, None) == INVALID
     assert lib.moe_lora_group(P, 4, 4, P, None, None) == INVALID
     assert lib.moe_lora_group(P + 2, 4, 4, P, P, None) == MISALIGNED
+    assert lib.moe_lora_group(P, 4, 4, Q, P, None) == INVALID and lib.moe_lora_group(P, 4, 4, Q, P + 12, None) == INVALID
+    assert lib.moe_lora_group(P, 4, 4, P + 12, Q, None) == INVALID and lib.moe_lora_group(P + 16, 4, 4, P, Q, None) == INVALID
+    assert lib.moe_lora_group(P, 4, 4, Q, Q + 16, None) == INVALID and lib.moe_lora_group(P, 4, 4, Q + 12, Q, None) == INVALID
     need = lib.moe_lora_add_workspace_bytes(10, 96, 128, 16, 3)
     good = dict(x=P, xs=128, M=10, K=128, N=96, R=16, L=3, a=P, b=P, sc=P, off=P, rows=P, yt=1, base=P, bs=96, y=Q, ys=96,
                 ws=P, n=need)
