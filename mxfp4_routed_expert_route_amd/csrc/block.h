@@ -71,7 +71,7 @@ struct LoraArgs {
   int64_t base_stride;
   void* y;
   int64_t y_stride;
-  float* v;                 // inner sums, [lora_splits][M][R]
+  float* v;                 // inner sums in the grouped order, [splits of K][M][R]
 };
 hipError_t launch_lora_add(const LoraArgs& a, bool f32, hipStream_t stream);
 // lora_tall.hip: sets *done, or leaves the call to others (few rows, R > 64).

@@ -13,7 +13,8 @@ constexpr int kMaxSequences = 1 << 20;
 constexpr int kLoraMaxN = 1 << 24;
 
 // moe_rms_norm_grad: most workgroups, each of which leaves one partial row of dweight: 2^18
-// threads, whose partial rows are 8 MB at most (16 beyond H = 16384).
+// threads, whose partial rows are 8 MB at most (16 beyond H = 16384).  2^17 / 2^18 / 2^19, us: 8191 x 4096
+// 69.6 / 56.3 / 64.5, 1000 x 4096 13.8 / 13.4 / 16.8, 65536 x 128 16.5 / 16.8 / 20.1, 2048 x 16384 77.5 / 63.2 / 70.6.
 inline int64_t norm_grad_groups(int64_t rows, int H) {
   int64_t threads = 256;   // of a row, or of several short ones
   while (threads < 1024 && threads * 8 < H) threads *= 2;
@@ -28,7 +29,8 @@ inline int64_t balance_slots(int64_t T, int n_seqs) {
 }
 // A sequence of more (token, slot) pairs is counted by a launch of its own, in chunks of at least
 // kCountChunk tokens, and has more than kLongTokens tokens: chunk c's counts of the sequence that
-// begins at token t are at slot c + t / kLongTokens, no two at one.
+// begins at token t are at slot c + t / kLongTokens, no two at one.  A border of 4096 / 8192 / 16384 pairs, us:
+// 65536 tokens of 256 experts, k = 8, in 64 sequences 42.2 / 42.5 / 47.1, 8191 tokens in 16 19.9 / 19.2 / 19.0.
 constexpr int kShortPairs = 8192, kLongTokens = kShortPairs / kMaxK, kCountChunk = 256;
 inline int64_t balance_count_slots(int64_t T) { return T / kCountChunk + T / kLongTokens + 2; }
 

