@@ -15,7 +15,7 @@
 // Bound by memory and its requests: 8191 x 4096 x 4096, rank 64, 8 adapters, moves 226 MB by the
 // counters (x, base and y once each are 201) in 54 us, 4.2 TB/s, where a copy reaches 5.1; the inner sums
 // take about 21 us of that, and with one workgroup a CU the two parts do not overlap.  MFMAs are busy
-// 0.14 of the time.  Rank 16 takes 51 us, fp32 base and y (402 MB) 85; the two launches of lora.hip 87 at
+// 0.14 of the time.  Rank 16 takes 51 us, fp32 base and y (402 MB) 85; the two launches of lora.hip 94 at
 // rank 64.  Tried without gain: 16 wavefronts (spills), columns begun at another place by each
 // workgroup, non-temporal copies of x.
 #include <atomic>
@@ -373,8 +373,8 @@ hipError_t launch_lora_tall(const LoraArgs& a, bool f32, int wide, hipStream_t s
   int64_t rounds = (a.M + most * groups + most * kCus - 1) / (most * kCus);
   const int64_t rows = (a.M + rounds * kCus - groups - 1) / (rounds * kCus - groups);
   // Fewer rows a tile than this read the weights too often for one launch.  One launch / two (us, K = N =
-  // 4096, 8 adapters): rank 16, 2048 rows 27.5 / 23.6, 4096 36.4 / 37.1, 8191 51.5 / 55.7; rank 64, 2048
-  // 37.4 / 42.7, 4096 42.6 / 56.8, 8191 55.1 / 87.0.
+  // 4096, 8 adapters): rank 16, 2048 rows 28.0 / 24.1, 4096 36.8 / 35.8, 8191 51.7 / 55.7, 32768 178 / 187; rank 32, 2048
+  // 28.6 / 28.9, 4096 34.4 / 42.1; rank 64, 1024 36.7 / 30.1, 2048 37.8 / 40.5, 4096 43.0 / 58.6, 8191 54.9 / 94.1.
   const int least = a.R > 32 ? 9 : 17;
   if (rounds * kCus <= groups || rows < least || rows > most) return hipSuccess;
   const int64_t tiles = (a.M + (rows - 1) * groups) / rows;
