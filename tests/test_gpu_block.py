@@ -490,7 +490,7 @@ def group(ids, L):
 
 
 @pytest.mark.parametrize("M,L", [(0, 3), (1, 1), (5, 2), (63, 64), (64, 1), (65, 7), (512, 64), (1000, 1024), (1025, 700),
-                                 (1024, 3), (1026, 3), (8191, 8), (20000, 300), (300000, 5), (400001, 900)])
+                                 (1024, 3), (1026, 3), (8191, 8), (20000, 300), (70000, 895), (300000, 5), (400001, 900)])
 def test_lora_group(M, L):
     r = np.random.default_rng(M + L)
     for ids in (r.integers(-1, L, size=M), np.full(M, L - 1), np.full(M, -1), np.sort(r.integers(-2, L + 2, size=M)),
