@@ -3,17 +3,26 @@
 // A row stays in registers from its one load to the stores.  With z = s w (exact in fp32 for
 // bf16 weights) and y = z rstd, rstd is the same for a whole run of 128, so the codes are
 // E4M3(448 z / max |z|): they do not wait for rstd and carry none of its rounding.  Only a run
-// whose y, or z, lies below the format's floor of 2^-100 is quantised from y.
+// whose y, or z, lies below the format's floor of 2^-100 is quantised from y.  A row whose squares are
+// too large for fp32 is multiplied by 2^-100 (norm_core.h), which its small elements must not be before
+// they meet rstd: its y are s rstd 2^-100 w, in this order.
 //
 // Bound by memory: with the residual and both outputs an element moves 9 bytes, 8191 x 4096 302 MB
 // in 57 us (5.3 TB/s, a large copy 5.1; counters show no byte read or written twice).  A single row is
 // its launch and one chain of load, sum and store: kernel 3.3 us, the host's call 5.6.
+#include <type_traits>
+
 #include "block.h"
 #include "fp8_common.h"
 #include "norm_core.h"
 
 namespace moe {
 namespace {
+
+__device__ __forceinline__ uint32_t max_magnitude(uint32_t m, float v) {
+  const uint32_t b = __float_as_uint(v) & 0x7FFFFFFFu;
+  return b > m ? b : m;
+}
 
 template <int kLanes, int C>
 __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs a) {
@@ -74,44 +83,56 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
     ss = row_sum<kLanes>(ss, lds[1]);
   }
   const float rstd = row_rstd(ss.x, a.H, a.eps, f);
+  auto finish = [&](auto small_elements) {
+    constexpr bool kSmall = decltype(small_elements)::value;
 #pragma unroll
-  for (int i = 0; i < C; ++i) {
-    const int col = 8 * (t + T * i);
-    const bool here = col < H;
-    float z[8], y[8], w[8];
-    unpack_bf16x8(s[i], z);
+    for (int i = 0; i < C; ++i) {
+      const int col = 8 * (t + T * i);
+      const bool here = col < H;
+      float z[8], y[8], w[8];
+      unpack_bf16x8(s[i], z);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = 0.f;
-    if (here) load_weight8(a.w, a.w_f32, col, w);
-    uint32_t m = 0;   // largest |z|, on the bits
+      for (int j = 0; j < 8; ++j) w[j] = 0.f;
+      if (here) load_weight8(a.w, a.w_f32, col, w);
+      uint32_t m = 0;   // largest |z|, on the bits
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      z[j] = z[j] * f * w[j];
-      y[j] = z[j] * rstd;
-      const uint32_t b = __float_as_uint(z[j]) & 0x7FFFFFFFu;
-      m = b > m ? b : m;
-    }
-    if (a.y != nullptr && here) *reinterpret_cast<uint4*>(a.y + at + col) = pack_bf16x8(y);
-    if (a.q != nullptr) {   // uniform
-      m = row16_max_u32(m);
-      const float zmax = __uint_as_float(m);
-      float amax = zmax * rstd;
-      const bool finite = amax < __builtin_inff();   // false for NaN
-      amax = finite ? fmaxf(amax, 0x1p-100f) : 1.0f;
-      const bool direct = zmax >= 0x1p-100f && zmax * rstd >= 0x1p-100f && zmax < __builtin_inff();
-      const RunScale r = run_scale(direct ? zmax : amax);
+      for (int j = 0; j < 8; ++j) {
+        const float u = z[j];
+        z[j] = u * f * w[j];
+        y[j] = kSmall ? u * rstd * f * w[j] : z[j] * rstd;
+        m = max_magnitude(m, z[j]);
+      }
+      if (a.y != nullptr && here) *reinterpret_cast<uint4*>(a.y + at + col) = pack_bf16x8(y);
+      if (a.q != nullptr) {   // uniform
+        const float zmax = __uint_as_float(row16_max_u32(m));
+        float amax = zmax * rstd;
+        const bool direct = zmax >= 0x1p-100f && amax >= 0x1p-100f && zmax < __builtin_inff();
+        if (kSmall && !direct) {   // uniform over the run
+          m = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = run_quotient(direct ? z[j] : y[j], r);
-      uint2 o = make_uint2(pack_e4m3(y[0], y[1], y[2], y[3]), pack_e4m3(y[4], y[5], y[6], y[7]));
-      if (!finite) o.x = o.y = kNanCodes;
-      if (here) {
-        *reinterpret_cast<uint2*>(a.q + at + col) = o;
-        if ((t & 15) == 0)
-          a.scale[row * ((a.H + kFp8Block - 1) / kFp8Block) + col / kFp8Block] =
-              finite ? amax / 448.0f : __uint_as_float(0x7FC00000u);
+          for (int j = 0; j < 8; ++j) m = max_magnitude(m, y[j]);
+          amax = __uint_as_float(row16_max_u32(m));
+        }
+        const bool finite = amax < __builtin_inff();   // false for NaN
+        amax = finite ? fmaxf(amax, 0x1p-100f) : 1.0f;
+        const RunScale r = run_scale(direct ? zmax : amax);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = run_quotient(direct ? z[j] : y[j], r);
+        uint2 o = make_uint2(pack_e4m3(y[0], y[1], y[2], y[3]), pack_e4m3(y[4], y[5], y[6], y[7]));
+        if (!finite) o.x = o.y = kNanCodes;
+        if (here) {
+          *reinterpret_cast<uint2*>(a.q + at + col) = o;
+          if ((t & 15) == 0)
+            a.scale[row * ((a.H + kFp8Block - 1) / kFp8Block) + col / kFp8Block] =
+                finite ? amax / 448.0f : __uint_as_float(0x7FC00000u);
+        }
       }
     }
-  }
+  };
+  if (f < 1.0f)   // uniform over the threads of a row
+    finish(std::true_type{});
+  else
+    finish(std::false_type{});
 }
 
 template <int kLanes, int C>

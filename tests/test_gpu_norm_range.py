@@ -1,0 +1,46 @@
+"""The norm where fp32 products leave their range on the way to results within it.
+
+Tolerances as in test_gpu_block.py: bf16 results half a step, NORM for the fp32 in front of them.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import block
+from tests.test_gpu_block import DEV, HALF, NORM, U, close, f64, gen, norm, randn
+
+pytestmark = pytest.mark.gpu
+
+
+def check(x, w, eps, out):
+    """y, and the FP8 output by what it stands for: runs of small values are quantised from y."""
+    _, y = block.rms_norm(f64(x), None, f64(w), eps)
+    H = x.shape[1]
+    close(out["y"], y, np.abs(y) * (HALF + NORM) + 2.0 ** -133, "y")
+    amax = np.maximum.reduceat(np.abs(y), np.arange(0, H, 128), axis=1)
+    scale = np.maximum(amax, 2.0 ** -100) / 448.0
+    close(out["scale"], scale, scale * (NORM + 2 * U), "scale")
+    each = np.repeat(scale, 128, axis=1)[:, :H]
+    back = f64(out["q"].float()) * np.repeat(f64(out["scale"]), 128, axis=1)[:, :H]
+    # half a step of E4M3 relative, half its smallest step below 2^-6 of the scale's unit
+    close(back, y, np.abs(y) * (2.0 ** -4 + 2 * NORM) + each * 2.0 ** -10 * 1.01, "q")
+
+
+SIZES = [64, 208, 400, 1024, 4096, 16400, 65536]   # every number of lanes and chunks of a row
+
+
+@pytest.mark.parametrize("H", SIZES)
+@pytest.mark.parametrize("wtype", [torch.bfloat16, torch.float32])
+def test_norm_of_one_huge_element_among_small_ones(H, wtype):
+    """A row whose squares leave fp32, with elements whose products are below it until they meet 1 / rms."""
+    g = gen(H)
+    x = torch.rand(5, H, generator=g) + 1.0
+    for i, (huge, small) in enumerate([(52, -45), (52, -50), (127, 30), (60, -40), (100, -20)]):
+        x[i] *= 2.0 ** small
+        x[i, (7 * i) % H] = 2.0 ** huge
+    x = x.bfloat16().to(DEV)
+    w = randn(g, H, dtype=wtype)
+    for eps in (0.0, 1e-6):
+        check(x, w, eps, norm(x, w, eps, None, y=True, q=True))
