@@ -5,7 +5,8 @@
 // E4M3(448 z / max |z|): they do not wait for rstd and carry none of its rounding.  Only a run
 // whose y, or z, lies below the format's floor of 2^-100 is quantised from y.  A row whose squares are
 // too large for fp32 is multiplied by 2^-100 (norm_core.h), which its small elements must not be before
-// they meet rstd: its y are s rstd 2^-100 w, in this order.
+// they meet rstd: its y are s rstd 2^-100 w, in this order.  Where s w overflows (weights of 2^78 or more),
+// what was stored is stored again, from s rstd w.
 //
 // Bound by memory: with the residual and both outputs an element moves 9 bytes, 8191 x 4096 302 MB
 // in 57 us (5.3 TB/s, a large copy 5.1; counters show no byte read or written twice).  A single row is
@@ -83,13 +84,17 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
     ss = row_sum<kLanes>(ss, lds[1]);
   }
   const float rstd = row_rstd(ss.x, a.H, a.eps, f);
-  auto finish = [&](auto small_elements) {
-    constexpr bool kSmall = decltype(small_elements)::value;
+  // Returns whether s f w overflowed, in any of the thread's runs (without q, elements).
+  auto finish = [&](auto in_range) {
+    constexpr bool kInRange = decltype(in_range)::value;
+    uint32_t largest = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int col = 8 * (t + T * i);
       const bool here = col < H;
       float z[8], y[8], w[8];
+      // without this the compiler keeps the elements unpacked from the first pass on, in twice the registers
+      if (!kInRange) asm("" : "+v"(s[i].x), "+v"(s[i].y), "+v"(s[i].z), "+v"(s[i].w));
       unpack_bf16x8(s[i], z);
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = 0.f;
@@ -99,19 +104,22 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
       for (int j = 0; j < 8; ++j) {
         const float u = z[j];
         z[j] = u * f * w[j];
-        y[j] = kSmall ? u * rstd * f * w[j] : z[j] * rstd;
+        y[j] = z[j] * rstd;
+        if (!kInRange && (f < 1.0f || !(fabsf(z[j]) < __builtin_inff())))
+          y[j] = (f < 1.0f ? u * rstd * f : u * f * rstd) * w[j];
         m = max_magnitude(m, z[j]);
       }
       if (a.y != nullptr && here) *reinterpret_cast<uint4*>(a.y + at + col) = pack_bf16x8(y);
       if (a.q != nullptr) {   // uniform
-        const float zmax = __uint_as_float(row16_max_u32(m));
+        m = row16_max_u32(m);
+        const float zmax = __uint_as_float(m);
         float amax = zmax * rstd;
         const bool direct = zmax >= 0x1p-100f && amax >= 0x1p-100f && zmax < __builtin_inff();
-        if (kSmall && !direct) {   // uniform over the run
-          m = 0;
+        if (!kInRange && !direct) {   // uniform over the run
+          uint32_t top = 0;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) m = max_magnitude(m, y[j]);
-          amax = __uint_as_float(row16_max_u32(m));
+          for (int j = 0; j < 8; ++j) top = max_magnitude(top, y[j]);
+          amax = __uint_as_float(row16_max_u32(top));
         }
         const bool finite = amax < __builtin_inff();   // false for NaN
         amax = finite ? fmaxf(amax, 0x1p-100f) : 1.0f;
@@ -127,12 +135,13 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
                 finite ? amax / 448.0f : __uint_as_float(0x7FC00000u);
         }
       }
+      largest = m > largest ? m : largest;
     }
+    return largest >= 0x7F800000u;
   };
-  if (f < 1.0f)   // uniform over the threads of a row
-    finish(std::true_type{});
-  else
-    finish(std::false_type{});
+  bool out_of_range = f < 1.0f;   // uniform over the threads of a row
+  if (!out_of_range) out_of_range = finish(std::true_type{});
+  if (out_of_range) finish(std::false_type{});
 }
 
 template <int kLanes, int C>

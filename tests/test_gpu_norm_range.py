@@ -44,3 +44,20 @@ def test_norm_of_one_huge_element_among_small_ones(H, wtype):
     w = randn(g, H, dtype=wtype)
     for eps in (0.0, 1e-6):
         check(x, w, eps, norm(x, w, eps, None, y=True, q=True))
+
+
+@pytest.mark.parametrize("H", SIZES)
+@pytest.mark.parametrize("wtype", [torch.bfloat16, torch.float32])
+def test_norm_of_large_rows_by_large_weights(H, wtype):
+    """s w is past fp32's largest value, s w / rms is not; beside runs where neither is."""
+    g = gen(H + 1)
+    x = torch.randn(3, H, generator=g)
+    for i, size in enumerate([45, 40, 0]):
+        x[i] *= 2.0 ** size
+    x = x.bfloat16().to(DEV)
+    w = torch.randn(H, generator=g)
+    w[: H // 2 : 3] *= 2.0 ** 100
+    w = w.to(wtype).to(DEV)
+    check(x, w, 1e-6, norm(x, w, 1e-6, None, y=True, q=True))
+    y = norm(x, w, 1e-6, None, y=True, q=False)["y"]
+    assert torch.equal(y, norm(x, w, 1e-6, None, y=True, q=True)["y"])
