@@ -72,17 +72,16 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_grad_kernel(NormGrad
       load_weights(i, w);
     }
   };
-  auto both = [&](const GradRow<C>& r, int64_t row, float f) {
-    float2 v = make_float2(0.f, 0.f);   // of s^2, of z s
+  auto both = [&](const GradRow<C>& r, int64_t row, float f, float fz) {
+    float2 v = make_float2(0.f, 0.f);   // of (f s)^2, of z (fz s)
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float u[8], d[8], e[8], w[8];
       chunk(r, row, i, u, d, e, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        u[j] *= f;
-        v.x = fmaf(u[j], u[j], v.x);
-        v.y = fmaf(d[j] * w[j], u[j], v.y);
+        v.x = fmaf(u[j] * f, u[j] * f, v.x);
+        v.y = fmaf(d[j] * w[j], u[j] * fz, v.y);
       }
     }
     return v;
@@ -95,16 +94,26 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_grad_kernel(NormGrad
     if constexpr (kKeep)
 #pragma unroll
       for (int i = 0; i < C; ++i) load(row, i, r.s[i], r.g[i], r.e[i]);
-    float2 v = row_sum<kLanes>(both(r, row, 1.0f), sums[turn]);   // two in turn: one barrier a row
+    float2 v = row_sum<kLanes>(both(r, row, 1.0f, 1.0f), sums[turn]);   // two in turn: one barrier a row
     turn ^= 1;
     const float f = row_factor(v.x, a.eps);
+    // Products with the 2^-100 of a row that has a huge element would leave fp32's range beside it: the
+    // sum of z s takes half of the exponent, and s meets rstd first.
+    const float fz = f < 1.0f ? 0x1p-50f : f;
     if (f != 1.0f) {   // uniform over the threads of a row
-      v = row_sum<kLanes>(both(r, row, f), sums[2]);
+      if constexpr (kKeep)   // as loaded, not as unpacked before: in half of the registers
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+          asm("" : "+v"(r.s[i].x), "+v"(r.s[i].y), "+v"(r.s[i].z), "+v"(r.s[i].w));
+          asm("" : "+v"(r.g[i].x), "+v"(r.g[i].y), "+v"(r.g[i].z), "+v"(r.g[i].w));
+        }
+      v = row_sum<kLanes>(both(r, row, f, fz), sums[2]);
       if constexpr (kLanes == 0) __syncthreads();   // sums[2] may be next in line too
     }
     // a row that is not there adds zeros (its zeros with an eps of 0 would be NaN)
     const float rstd = row < a.rows ? row_rstd(v.x, a.H, a.eps, f) : 0.f;
-    const float c = rstd * v.y / static_cast<float>(a.H);   // mean(z u)
+    const float c = (f < 1.0f ? rstd * fz : rstd) * v.y / static_cast<float>(a.H);   // mean(z u)
+    const float first = f < 1.0f ? rstd : f, second = f < 1.0f ? f : rstd;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int col = 8 * (t + T * i);
@@ -112,9 +121,9 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_grad_kernel(NormGrad
       chunk(r, row, i, u, d, e, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        u[j] = u[j] * f * rstd;
+        u[j] = u[j] * first * second;
         acc[i][j] = fmaf(d[j], u[j], acc[i][j]);
-        d[j] = fmaf(f * rstd, fmaf(-u[j], c, d[j] * w[j]), e[j]);
+        d[j] = fmaf(first * second, fmaf(-u[j], c, d[j] * w[j]), e[j]);
       }
       if (a.dx != nullptr && row < a.rows && col < a.H)
         *reinterpret_cast<uint4*>(a.dx + row * a.H + col) = pack_bf16x8(d);

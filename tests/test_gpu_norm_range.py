@@ -1,4 +1,4 @@
-"""The norm where fp32 products leave their range on the way to results within it.
+"""The norm and its gradient where fp32 products leave their range on the way to results within it.
 
 Tolerances as in test_gpu_block.py: bf16 results half a step, NORM for the fp32 in front of them.
 """
@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import block
-from tests.test_gpu_block import DEV, HALF, NORM, U, close, f64, gen, norm, randn
+from tests.test_gpu_block import DEV, HALF, NORM, U, check_norm_grad, close, f64, gen, norm, norm_grad, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +61,24 @@ def test_norm_of_large_rows_by_large_weights(H, wtype):
     check(x, w, 1e-6, norm(x, w, 1e-6, None, y=True, q=True))
     y = norm(x, w, 1e-6, None, y=True, q=False)["y"]
     assert torch.equal(y, norm(x, w, 1e-6, None, y=True, q=True)["y"])
+
+
+@pytest.mark.parametrize("H", SIZES)
+def test_norm_grad_of_one_huge_element_among_small_ones(H):
+    g = gen(H + 2)
+    s = torch.rand(4, H, generator=g) + 1.0
+    for i, (huge, small) in enumerate([(52, -45), (52, -50), (127, 30), (60, -40)]):
+        s[i] *= 2.0 ** small
+        s[i, 3] = 2.0 ** huge
+    s = s.bfloat16().to(DEV)
+    w = randn(g, H)
+    dy = randn(g, 4, H)
+    dy[:, 3] = 0.0       # no large term in any sum
+    dx, dw = norm_grad(s, w, 0.0, dy)
+    check_norm_grad(s, w, 0.0, dy, None, dx, dw)
+    for i in range(4):   # a weight's gradient of one row alone
+        dx, dw = norm_grad(s[i:i + 1], w, 0.0, dy[i:i + 1])
+        check_norm_grad(s[i:i + 1], w, 0.0, dy[i:i + 1], None, dx, dw)
+    dy *= 2.0 ** 30      # the mean of the small terms reaches the huge element's dx
+    dx, dw = norm_grad(s[:1], w, 0.0, dy[:1])
+    check_norm_grad(s[:1], w, 0.0, dy[:1], None, dx, dw)
