@@ -114,6 +114,9 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_grad_kernel(NormGrad
     const float rstd = row < a.rows ? row_rstd(v.x, a.H, a.eps, f) : 0.f;
     const float c = (f < 1.0f ? rstd * fz : rstd) * v.y / static_cast<float>(a.H);   // mean(z u)
     const float first = f < 1.0f ? rstd : f, second = f < 1.0f ? f : rstd;
+    // 1 / rms in two factors where it is past fp32's largest value (subnormal rows without eps)
+    const bool large = first * second >= 0x1p120f;
+    const float outer = large ? first : first * second, inner = large ? second : 1.0f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int col = 8 * (t + T * i);
@@ -123,7 +126,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_grad_kernel(NormGrad
       for (int j = 0; j < 8; ++j) {
         u[j] = u[j] * first * second;
         acc[i][j] = fmaf(d[j], u[j], acc[i][j]);
-        d[j] = fmaf(first * second, fmaf(-u[j], c, d[j] * w[j]), e[j]);
+        d[j] = fmaf(outer, inner * fmaf(-u[j], c, d[j] * w[j]), e[j]);
       }
       if (a.dx != nullptr && row < a.rows && col < a.H)
         *reinterpret_cast<uint4*>(a.dx + row * a.H + col) = pack_bf16x8(d);

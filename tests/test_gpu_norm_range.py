@@ -82,3 +82,18 @@ def test_norm_grad_of_one_huge_element_among_small_ones(H):
     dy *= 2.0 ** 30      # the mean of the small terms reaches the huge element's dx
     dx, dw = norm_grad(s[:1], w, 0.0, dy[:1])
     check_norm_grad(s[:1], w, 0.0, dy[:1], None, dx, dw)
+
+
+@pytest.mark.parametrize("H", SIZES)
+def test_norm_grad_of_subnormal_rows(H):
+    """Without eps 1 / rms is past fp32's largest value; dx is not."""
+    g = gen(H + 3)
+    s = (torch.randint(-7, 8, (4, H), generator=g).float() * 2.0 ** -133)
+    s[:, 0] = 2.0 ** -132
+    s = s.bfloat16().to(DEV)
+    w = randn(g, H)
+    dy, dsum = randn(g, 4, H, scale=2.0 ** -30), randn(g, 4, H)
+    dy[1] = 0.0
+    dx, dw = norm_grad(s, w, 0.0, dy, dsum)
+    check_norm_grad(s, w, 0.0, dy, dsum, dx, dw)
+    assert torch.equal(dx[1], dsum[1])
