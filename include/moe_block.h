@@ -146,7 +146,7 @@ moe_status moe_lora_group(const int32_t* adapter, int64_t M, int32_t L, int32_t*
  * and y[m] = base[m] for a row without an adapter (base NULL: 0 in its place).  base is the shared
  * projection's result, moe_gemm_fp8's y for one.  Inner sums are fp32 of exact products; they enter
  * the second product whole for an fp32 y, within 2^-17 of themselves for a bf16 one; y is rounded
- * once.
+ * once.  An infinite weight makes an infinity or a NaN as the formula does, of no other row.
  *
  *   x        bf16 [M][K], x_stride between rows    16-byte aligned
  *   a        bf16 [L][R][K]                        16-byte aligned

@@ -355,6 +355,21 @@ __global__ __launch_bounds__(256, KS <= 2 ? 4 : KS == 4 ? 3 : 2) void expand_ker
 #pragma unroll
       for (int f = 0; f < 4; ++f) *reinterpret_cast<floatx4*>(mine + r16 * kPitch + 16 * f + 4 * g) = acc[f];
       wave_sync_lds();
+      if (any_nan(acc, true)) {   // uniform
+        const int n = cur.n0 + lane;
+#pragma unroll 1
+        for (int r = 0; r < cur.tile.rows; ++r) {
+          float* at = mine + r * kPitch + lane;
+          const float* v = a.v + static_cast<int64_t>(cur.tile.begin + r) * a.R;
+          auto inner = [&](int k) {
+            float s = 0.f;
+            for (int q = 0; q < splits; ++q) s += v[static_cast<int64_t>(q) * a.M * a.R + k];
+            return s;
+          };
+          if (n < a.N && *at != *at) *at = whole_product(inner, a.b + (static_cast<int64_t>(w_adapter) * a.N + n) * a.R, a.R);
+        }
+        wave_sync_lds();
+      }
 #pragma unroll
       for (int i = 0; i < kGoes; ++i) {
         const float* from = mine + (kRows * i + lane / kLanes) * kPitch + my_col;
@@ -443,7 +458,7 @@ __global__ __launch_bounds__(1024) void small_kernel(LoraArgs a, int col_blocks,
     if constexpr (NF == 4) __syncthreads();
     if (wave < 2 * KS) *reinterpret_cast<floatx4*>(&sums[r16 * kPitch + 16 * wave + 4 * g]) = total;
     __syncthreads();
-    floatx4 d = {0.f, 0.f, 0.f, 0.f};
+    floatx4 d[1] = {floatx4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
     for (int s = 0; s < KS; ++s) {
       float v[8];
@@ -451,10 +466,17 @@ __global__ __launch_bounds__(1024) void small_kernel(LoraArgs a, int col_blocks,
       bf16x8 q[kParts];
       split<kParts>(v, q);
 #pragma unroll
-      for (int i = 0; i < kParts; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s], q[i], d, 0, 0, 0);
+      for (int i = 0; i < kParts; ++i) d[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s], q[i], d[0], 0, 0, 0);
     }
-    cols.put4(0, fmaf(scaling, d[0], cols.get(0)), fmaf(scaling, d[1], cols.get(1)), fmaf(scaling, d[2], cols.get(2)),
-              fmaf(scaling, d[3], cols.get(3)));
+    if (any_nan(d, true)) {   // uniform
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (j < left && d[0][j] != d[0][j])
+          d[0][j] = whole_product([&](int r) { return sums[r16 * kPitch + r]; },
+                                  a.b + (static_cast<int64_t>(tile.adapter) * a.N + c0 + j) * a.R, a.R);
+    }
+    cols.put4(0, fmaf(scaling, d[0][0], cols.get(0)), fmaf(scaling, d[0][1], cols.get(1)),
+              fmaf(scaling, d[0][2], cols.get(2)), fmaf(scaling, d[0][3], cols.get(3)));
   }
   if (out) cols.store(y + row * a.y_stride + c0, left, whole);
 }

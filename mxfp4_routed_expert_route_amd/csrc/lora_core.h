@@ -119,6 +119,24 @@ __device__ __forceinline__ void split(const float (&v)[8], bf16x8 (&part)[kParts
     part[kParts - 1][j] = static_cast<__bf16>(left);
   }
 }
+// Infinite weights: the first part of an inner sum makes of one what the sum does, but a lower part may be
+// 0, and 0 times an infinity is NaN.  So results that are NaN are made again from whole inner sums, one by
+// one: few results, or ones that stay NaN.  `here`: the lane's results are any row's.
+template <int n>
+__device__ __forceinline__ bool any_nan(const floatx4 (&v)[n], bool here) {   // over the wavefront
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < n; ++i) s += (v[i][0] + v[i][1]) + (v[i][2] + v[i][3]);
+  return __builtin_amdgcn_ballot_w64(here && s != s) != 0ull;
+}
+// sum_r v(r) b[r], up to the first NaN: one in an inner sum, of a row that holds one, costs a term.
+template <class Inner>
+__device__ __forceinline__ float whole_product(Inner v, const uint16_t* b, int R) {
+  float s = 0.f;
+#pragma unroll 1
+  for (int r = 0; r < R && s == s; ++r) s = fmaf(v(r), bf16_bits_to_f32(b[r]), s);
+  return s;
+}
 template <class Out>
 constexpr int kPartsOf = sizeof(Out) == 4 ? 3 : 2;
 

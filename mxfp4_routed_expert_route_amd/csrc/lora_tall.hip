@@ -266,6 +266,23 @@ __global__ __launch_bounds__(512, 2) void tall_kernel(LoraArgs a, int tile_rows,
           for (int f = 0; f < 4; ++f)
             *reinterpret_cast<floatx4*>(exchange + r16 * S::kPitch + 16 * f + 4 * g) = acc[f];
           wave_sync_lds();
+          if (any_nan(acc, 16 * m + r16 < tile.rows)) {   // uniform
+            const int in_m = tile.rows - 16 * m < 16 ? tile.rows - 16 * m : 16, n = n0 + lane;
+#pragma unroll 1
+            for (int i = 0; i < in_m; ++i) {
+              const int r = 16 * m + i;
+              float* at = exchange + i * S::kPitch + lane;
+              auto inner = [&](int k) {
+                const int c = k >> 3;
+                const unsigned char* from = tall_lds + r * (KS * 64) + 16 * (KS == 2 ? c ^ ((r >> 1) & 7) : c) + 2 * (k & 7);
+                float s = 0.f;
+                for (int q = 0; q < kParts; ++q) s += bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(from + q * S::part));
+                return s;
+              };
+              if (n < a.N && *at != *at) *at = whole_product(inner, weights + static_cast<int64_t>(n) * a.R, a.R);
+            }
+            wave_sync_lds();
+          }
 #pragma unroll
           for (int i = 0; i < kGoes; ++i)
 #pragma unroll
