@@ -164,8 +164,8 @@ __global__ __launch_bounds__(512, 2) void tall_kernel(LoraArgs a, int tile_rows,
           float d[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            d[j] = p + 1 < kParts ? __uint_as_float(__float_as_uint(left[j]) & 0xFFFF0000u) : left[j];
-            if (p + 1 < kParts) left[j] = fabsf(d[j]) < __builtin_inff() ? left[j] - d[j] : 0.f;
+            d[j] = p + 1 < kParts ? upper_part<kParts>(left[j]) : left[j];
+            if (p + 1 < kParts) left[j] = lower_part(left[j], d[j]);
           }
           *reinterpret_cast<uint2*>(to + p * S::part) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
         }
