@@ -14,9 +14,10 @@
 
 namespace moe {
 
-// What a row with the sum of squares `ss` is multiplied by; 1 for all but extreme rows.
+// What a row with the sum of squares `ss` is multiplied by; 1 for all but extreme rows.  2^-74 is the
+// largest that keeps the squares of 65536 elements in range, so that the least is lost of small ones.
 __device__ __forceinline__ float row_factor(float ss, float eps) {
-  if (!(ss <= 0x1p100f)) return 0x1p-100f;
+  if (!(ss <= 0x1p100f)) return 0x1p-74f;
   return ss < 0x1p-80f && eps < 0x1p-60f ? 0x1p100f : 1.0f;
 }
 

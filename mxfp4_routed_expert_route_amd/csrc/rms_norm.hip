@@ -4,9 +4,10 @@
 // bf16 weights) and y = z rstd, rstd is the same for a whole run of 128, so the codes are
 // E4M3(448 z / max |z|): they do not wait for rstd and carry none of its rounding.  Only a run
 // whose y, or z, lies below the format's floor of 2^-100 is quantised from y.  A row whose squares are
-// too large for fp32 is multiplied by 2^-100 (norm_core.h), which its small elements must not be before
-// they meet rstd: its y are s rstd 2^-100 w, in this order.  Where s w overflows (weights of 2^78 or more),
-// what was stored is stored again, from s rstd w.
+// too large for fp32 is multiplied by 2^-74 (norm_core.h), which its small elements must not be before
+// they meet rstd: its y are s rstd 2^-74 w, in this order.  Where s w overflows (weights of 2^78 or more),
+// what was stored is stored again, from s rstd w.  Other rows pay for that 0.2 to 0.8 us of 28 to 58 at
+// 8191 x 4096, with their elements packed until the end.
 //
 // Bound by memory: with the residual and both outputs an element moves 9 bytes, 8191 x 4096 302 MB
 // in 57 us (5.3 TB/s, a large copy 5.1; counters show no byte read or written twice).  A single row is
@@ -72,7 +73,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
   }
   ss = row_sum<kLanes>(ss, lds[0]);
   const float f = row_factor(ss.x, a.eps);
-  if (f != 1.0f) {   // uniform over the threads of a row
+  if (__builtin_expect(f != 1.0f, false)) {   // uniform over the threads of a row
     ss.x = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
@@ -83,18 +84,18 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
     }
     ss = row_sum<kLanes>(ss, lds[1]);
   }
-  const float rstd = row_rstd(ss.x, a.H, a.eps, f);
-  // Returns whether s f w overflowed, in any of the thread's runs (without q, elements).
+  // Returns whether s w overflowed, in any of the thread's runs (without q, elements).
   auto finish = [&](auto in_range) {
-    constexpr bool kInRange = decltype(in_range)::value;
+    constexpr bool kInRange = decltype(in_range)::value;   // f is 1, and s w expected below an infinity
+    const float rstd = row_rstd(ss.x, a.H, a.eps, kInRange ? 1.0f : f);
     uint32_t largest = 0;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int col = 8 * (t + T * i);
       const bool here = col < H;
       float z[8], y[8], w[8];
-      // without this the compiler keeps the elements unpacked from the first pass on, in twice the registers
-      if (!kInRange) asm("" : "+v"(s[i].x), "+v"(s[i].y), "+v"(s[i].z), "+v"(s[i].w));
+      // without this the compiler keeps the elements unpacked from the sum of squares on, in twice the registers
+      asm("" : "+v"(s[i].x), "+v"(s[i].y), "+v"(s[i].z), "+v"(s[i].w));
       unpack_bf16x8(s[i], z);
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = 0.f;
@@ -103,7 +104,7 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float u = z[j];
-        z[j] = u * f * w[j];
+        z[j] = (kInRange ? u : u * f) * w[j];
         y[j] = z[j] * rstd;
         if (!kInRange && (f < 1.0f || !(fabsf(z[j]) < __builtin_inff())))
           y[j] = (f < 1.0f ? u * rstd * f : u * f * rstd) * w[j];
@@ -139,9 +140,9 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void rms_norm_kernel(NormArgs 
     }
     return largest >= 0x7F800000u;
   };
-  bool out_of_range = f < 1.0f;   // uniform over the threads of a row
-  if (!out_of_range) out_of_range = finish(std::true_type{});
-  if (out_of_range) finish(std::false_type{});
+  bool out_of_range = f != 1.0f;   // uniform over the threads of a row
+  if (__builtin_expect(!out_of_range, true)) out_of_range = finish(std::true_type{});
+  if (__builtin_expect(out_of_range, false)) finish(std::false_type{});
 }
 
 template <int kLanes, int C>

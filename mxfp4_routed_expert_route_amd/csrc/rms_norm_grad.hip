@@ -40,9 +40,19 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_grad_kernel(NormGrad
     for (int j = 0; j < 8; ++j) w[j] = 0.f;
     if (col < a.H) load_weight8(a.w, a.w_f32, col, w);
   };
-  if constexpr (kKeep)
+  auto load_all_weights = [&]() {
+    if constexpr (kKeep)
 #pragma unroll
-    for (int i = 0; i < C; ++i) load_weights(i, weights[i]);
+      for (int i = 0; i < C; ++i) load_weights(i, weights[i]);
+  };
+  auto scale_weights = [&](float by) {
+    if constexpr (kKeep)
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) weights[i][j] *= by;
+  };
+  load_all_weights();
   auto load = [&](int64_t row, int i, uint4& s, uint4& g, uint4& e) {
     const int col = 8 * (t + T * i);
     s = g = e = make_uint4(0u, 0u, 0u, 0u);
@@ -72,16 +82,17 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_grad_kernel(NormGrad
       load_weights(i, w);
     }
   };
-  auto both = [&](const GradRow<C>& r, int64_t row, float f, float fz) {
-    float2 v = make_float2(0.f, 0.f);   // of (f s)^2, of z (fz s)
+  auto both = [&](const GradRow<C>& r, int64_t row, float f) {
+    float2 v = make_float2(0.f, 0.f);   // of s^2, of z s
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       float u[8], d[8], e[8], w[8];
       chunk(r, row, i, u, d, e, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        v.x = fmaf(u[j] * f, u[j] * f, v.x);
-        v.y = fmaf(d[j] * w[j], u[j] * fz, v.y);
+        u[j] *= f;
+        v.x = fmaf(u[j], u[j], v.x);
+        v.y = fmaf(d[j] * w[j], u[j], v.y);
       }
     }
     return v;
@@ -94,29 +105,25 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_grad_kernel(NormGrad
     if constexpr (kKeep)
 #pragma unroll
       for (int i = 0; i < C; ++i) load(row, i, r.s[i], r.g[i], r.e[i]);
-    float2 v = row_sum<kLanes>(both(r, row, 1.0f, 1.0f), sums[turn]);   // two in turn: one barrier a row
+    float2 v = row_sum<kLanes>(both(r, row, 1.0f), sums[turn]);   // two in turn: one barrier a row
     turn ^= 1;
     const float f = row_factor(v.x, a.eps);
-    // Products with the 2^-100 of a row that has a huge element would leave fp32's range beside it: the
-    // sum of z s takes half of the exponent, and s meets rstd first.
-    const float fz = f < 1.0f ? 0x1p-50f : f;
     if (f != 1.0f) {   // uniform over the threads of a row
-      if constexpr (kKeep)   // as loaded, not as unpacked before: in half of the registers
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-          asm("" : "+v"(r.s[i].x), "+v"(r.s[i].y), "+v"(r.s[i].z), "+v"(r.s[i].w));
-          asm("" : "+v"(r.g[i].x), "+v"(r.g[i].y), "+v"(r.g[i].z), "+v"(r.g[i].w));
-        }
-      v = row_sum<kLanes>(both(r, row, f, fz), sums[2]);
+      v = row_sum<kLanes>(both(r, row, f), sums[2]);
       if constexpr (kLanes == 0) __syncthreads();   // sums[2] may be next in line too
     }
     // a row that is not there adds zeros (its zeros with an eps of 0 would be NaN)
     const float rstd = row < a.rows ? row_rstd(v.x, a.H, a.eps, f) : 0.f;
-    const float c = (f < 1.0f ? rstd * fz : rstd) * v.y / static_cast<float>(a.H);   // mean(z u)
-    const float first = f < 1.0f ? rstd : f, second = f < 1.0f ? f : rstd;
-    // 1 / rms in two factors where it is past fp32's largest value (subnormal rows without eps)
-    const bool large = first * second >= 0x1p120f;
-    const float outer = large ? first : first * second, inner = large ? second : 1.0f;
+    // u = s p r, dx = r (p z - u c) + dsum: c is p mean(z u).  p is 1 but where 1 / rms is past fp32's largest
+    // value, in subnormal rows without eps.
+    float p = 1.0f, r1 = f * rstd, c = rstd * v.y / static_cast<float>(a.H);
+    const bool large = r1 >= 0x1p120f;
+    if (__builtin_expect(large, false)) {   // uniform over the threads of a row
+      p = 0x1p24f;   // 1 / rms is 2^141 at most
+      r1 = f * 0x1p-24f * rstd;
+      c *= p;
+      scale_weights(p);
+    }
 #pragma unroll
     for (int i = 0; i < C; ++i) {
       const int col = 8 * (t + T * i);
@@ -124,13 +131,15 @@ __global__ __launch_bounds__(kLanes ? 256 : 1024) void norm_grad_kernel(NormGrad
       chunk(r, row, i, u, d, e, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        u[j] = u[j] * first * second;
+        u[j] = u[j] * p * r1;
         acc[i][j] = fmaf(d[j], u[j], acc[i][j]);
-        d[j] = fmaf(outer, inner * fmaf(-u[j], c, d[j] * w[j]), e[j]);
+        if (!kKeep) w[j] *= p;
+        d[j] = fmaf(r1, fmaf(-u[j], c, d[j] * w[j]), e[j]);
       }
       if (a.dx != nullptr && row < a.rows && col < a.H)
         *reinterpret_cast<uint4*>(a.dx + row * a.H + col) = pack_bf16x8(d);
     }
+    if (__builtin_expect(large, false)) load_all_weights();
   }
   if (a.dw == nullptr) return;
   float* out = a.part + static_cast<int64_t>(blockIdx.x) * a.H;
