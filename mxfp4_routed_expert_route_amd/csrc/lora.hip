@@ -355,7 +355,7 @@ __global__ __launch_bounds__(256, KS <= 2 ? 4 : KS == 4 ? 3 : 2) void expand_ker
 #pragma unroll
       for (int f = 0; f < 4; ++f) *reinterpret_cast<floatx4*>(mine + r16 * kPitch + 16 * f + 4 * g) = acc[f];
       wave_sync_lds();
-      if (any_nan(acc, true)) {   // uniform
+      if (__builtin_expect(any_nan(acc, true), false)) {   // uniform
         const int n = cur.n0 + lane;
 #pragma unroll 1
         for (int r = 0; r < cur.tile.rows; ++r) {
@@ -468,7 +468,7 @@ __global__ __launch_bounds__(1024) void small_kernel(LoraArgs a, int col_blocks,
 #pragma unroll
       for (int i = 0; i < kParts; ++i) d[0] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[s], q[i], d[0], 0, 0, 0);
     }
-    if (any_nan(d, true)) {   // uniform
+    if (__builtin_expect(any_nan(d, true), false)) {   // uniform
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (j < left && d[0][j] != d[0][j])

@@ -103,21 +103,16 @@ __device__ __forceinline__ void load_f32x8(const float* p, float (&v)[8]) {
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// The first of kParts bf16 parts of v.  Three parts are the upper bits of what is left each time, the last one
-// rounded: together all 24 bits, for fp32 results.  Of two, the first is rounded as well, so that what
-// it leaves is half as much and they hold all but 2^-17 of v, far under a bf16 result's step
-// (cut off instead, they lack up to 2^-16).  Sums under 2^-110 hold fewer bits: lower parts are subnormal
-// there.  What rounds to an infinity without being one is cut off.
+// The first of kParts bf16 parts of v; what it leaves, v less that, is split further.  Three parts are the upper bits
+// of what is left each time, the last one rounded: together all 24 bits, for fp32 results.  Of two,
+// the first is rounded as well, so that what it leaves is half as much and they hold all but 2^-17 of v, far
+// under a bf16 result's step (cut off instead, they lack up to 2^-16).  Sums under 2^-110 hold
+// fewer bits: lower parts are subnormal there.  Of an infinity or NaN the last part is one, the others finite.
 template <int kParts>
 __device__ __forceinline__ float upper_part(float v) {
-  const float cut = __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
-  if constexpr (kParts > 2) return cut;
-  const float h = bf16_bits_to_f32(f32_to_bf16_bits(v));
-  return fabsf(h) == __builtin_inff() ? cut : h;
-}
-// What it leaves.
-__device__ __forceinline__ float lower_part(float v, float upper) {
-  return fabsf(upper) < __builtin_inff() ? v - upper : 0.f;
+  constexpr float kMost = kParts > 2 ? 0x1.fffffep+127f : 0x1.fep+127f;   // what does not become an infinity
+  v = __builtin_amdgcn_fmed3f(v, -kMost, kMost);
+  return kParts > 2 ? __uint_as_float(__float_as_uint(v) & 0xFFFF0000u) : bf16_bits_to_f32(f32_to_bf16_bits(v));
 }
 template <int kParts>
 __device__ __forceinline__ void split(const float (&v)[8], bf16x8 (&part)[kParts]) {
@@ -128,7 +123,7 @@ __device__ __forceinline__ void split(const float (&v)[8], bf16x8 (&part)[kParts
     for (int i = 0; i < kParts - 1; ++i) {
       const float h = upper_part<kParts>(left);
       part[i][j] = static_cast<__bf16>(h);
-      left = lower_part(left, h);
+      left -= h;
     }
     part[kParts - 1][j] = static_cast<__bf16>(left);
   }

@@ -165,7 +165,7 @@ __global__ __launch_bounds__(512, 2) void tall_kernel(LoraArgs a, int tile_rows,
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             d[j] = p + 1 < kParts ? upper_part<kParts>(left[j]) : left[j];
-            if (p + 1 < kParts) left[j] = lower_part(left[j], d[j]);
+            if (p + 1 < kParts) left[j] -= d[j];
           }
           *reinterpret_cast<uint2*>(to + p * S::part) = make_uint2(pack_bf16x2(d[0], d[1]), pack_bf16x2(d[2], d[3]));
         }
@@ -266,7 +266,7 @@ __global__ __launch_bounds__(512, 2) void tall_kernel(LoraArgs a, int tile_rows,
           for (int f = 0; f < 4; ++f)
             *reinterpret_cast<floatx4*>(exchange + r16 * S::kPitch + 16 * f + 4 * g) = acc[f];
           wave_sync_lds();
-          if (any_nan(acc, 16 * m + r16 < tile.rows)) {   // uniform
+          if (__builtin_expect(any_nan(acc, 16 * m + r16 < tile.rows), false)) {   // uniform
             const int in_m = tile.rows - 16 * m < 16 ? tile.rows - 16 * m : 16, n = n0 + lane;
 #pragma unroll 1
             for (int i = 0; i < in_m; ++i) {
