@@ -386,14 +386,18 @@ hipError_t launch_lora_tall(const LoraArgs& a, bool f32, int wide, hipStream_t s
   const int64_t groups = (a.M < a.L ? a.M : a.L) + 1;   // and the rows without an adapter
   const int64_t most = Tall<float, 4>::kRows;
   if (a.R > 64) return hipSuccess;
-  // the fewest rounds of at most kCus tiles that hold all the rows
-  int64_t rounds = (a.M + most * groups + most * kCus - 1) / (most * kCus);
+  // The fewest rounds of at most kCus tiles that hold all the rows: rounds kCus most >= M + most groups, so the
+  // rounds have more tiles than groups and the rows come to at most `most`.
+  const int64_t rounds = (a.M + most * groups + most * kCus - 1) / (most * kCus);
   const int64_t rows = (a.M + rounds * kCus - groups - 1) / (rounds * kCus - groups);
   // Fewer rows a tile than this read the weights too often for one launch.  One launch / two (us, K = N =
-  // 4096, 8 adapters): rank 16, 2048 rows 28.0 / 24.1, 4096 36.8 / 35.8, 8191 51.7 / 55.7, 32768 178 / 187; rank 32, 2048
-  // 28.6 / 28.9, 4096 34.4 / 42.1; rank 64, 1024 36.7 / 30.1, 2048 37.8 / 40.5, 4096 43.0 / 58.6, 8191 54.9 / 94.1.
-  const int least = a.R > 32 ? 9 : 17;
-  if (rounds * kCus <= groups || rows < least || rows > most) return hipSuccess;
+  // 4096, 8 adapters): rank 16, 2048 rows 28.2 / 22.9, 4096 37.1 / 34.0, 5000 40.2 / 41.0, 7000 45.6 / 48.4, 11000
+  // 61 / 72; rank 24, 4096 33.8 / 35.8; rank 32, 2048 29.0 / 27.6, 4096 34.5 / 38.5; rank 64, 1500 37.6 / 31.1, 2048
+  // 37.8 / 38.6, 3000 39.6 / 43.5.  The rule is not right everywhere: 33 or 34 rows a tile are a third fragment for
+  // one or two of them (rank 16, 8191 rows 52.7 / 51.0, 16384 121 / 101), and a rank of 8 gains by two
+  // launches up to some 8000 rows (5000 39.9 / 38.3, 9000 54.8 / 57.4).
+  const int least = a.R > 32 ? 9 : a.R > 16 ? 17 : 18;
+  if (rows < least) return hipSuccess;
   const int64_t tiles = (a.M + (rows - 1) * groups) / rows;
   if (tiles >= (int64_t{1} << 22)) return hipSuccess;   // fewer than 2^32 threads
   *done = true;

@@ -1,6 +1,6 @@
 """The operators around the layer at sizes where their launches grow or are cut: more tokens than a
 workgroup's smallest share times the launch, several long sequences side by side, more rows than one
-launch of the norm."""
+launch of the norm, rows at the borders of the adapters' forms."""
 from __future__ import annotations
 
 import numpy as np
@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from mxfp4_routed_expert_route_amd import binding
-from tests.test_gpu_block import DEV, FP8, balance, check_balance, check_norm, gen, randn
+from tests.test_gpu_block import DEV, FP8, balance, check_balance, check_lora, check_norm, gen, lora, randn, run_lora
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,14 @@ def test_norm_of_more_rows_than_a_launch(H):
         binding.moe_rms_norm(x[r0:r1], w, 1e-6, residual=r[r0:r1], **part)
         for n, t in part.items():
             assert torch.equal(t.view(torch.uint8), out[n][r0:r1].view(torch.uint8)), n
+
+
+@pytest.mark.parametrize("M,R", [(4199, 16), (4200, 16), (3952, 24), (3953, 24), (1976, 40), (1977, 40), (11856, 8), (11857, 8),
+                                 (11857, 64), (24144, 32), (24145, 16)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_lora_at_the_borders_of_one_launch(M, R, dtype):
+    """With 8 adapters: 17 and 18 (16 and 17, 8 and 9) rows a tile, the most rows of a round of tiles and one more."""
+    N, K, L = 72, 64, 8
+    ids = np.sort(np.random.default_rng(M).integers(-1, L, size=M))
+    x, a, b, s, base = lora(M, N, K, R, L, ids, M + R, dtype)
+    check_lora(x, a, b, s, ids, base, run_lora(x, a, b, s, ids, base, dtype))
