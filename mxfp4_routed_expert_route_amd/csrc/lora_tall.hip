@@ -182,8 +182,9 @@ __global__ __launch_bounds__(512, 2) void tall_kernel(LoraArgs a, int tile_rows,
   // and stores the same bits to the same place.
   constexpr int kPiece = 16 / sizeof(Out), kLanes = 64 / kPiece;   // columns of a lane, lanes of a row
   constexpr int kAt = 64 / kLanes, kGoes = 16 / kAt;               // rows of an access, accesses
-  const Out* base = a.base != nullptr ? static_cast<const Out*>(a.base) : static_cast<const Out*>(a.y);
-  const int64_t base_stride = a.base != nullptr ? a.base_stride : a.y_stride;
+  // Without a base what is loaded in its place is not used: one row of N * sizeof(Out) <= 2 N R bytes of B, from cache.
+  const Out* base = a.base != nullptr ? static_cast<const Out*>(a.base) : reinterpret_cast<const Out*>(a.b);
+  const int64_t base_stride = a.base != nullptr ? a.base_stride : 0;
   Out* y = static_cast<Out*>(a.y);
   const int my_row = lane / kLanes, my_col = kPiece * (lane % kLanes);
   float* exchange = reinterpret_cast<float*>(tall_lds + S::sums_at + wave * S::exchange);
