@@ -23,7 +23,9 @@ extern "C" {
  * Per row:
  *   s_i = bf16(x_i + residual_i)   (residual NULL: s = x)
  *   y_i = s_i * w_i / sqrt(mean_j s_j^2 + eps)
- * with statistics and products in fp32, at any magnitude of bf16 rows.  y is rounded once to bf16;
+ * with statistics and products in fp32, at any magnitude of bf16 rows and with elements of any other
+ * magnitude beside them; only a product s_i w_i under 2^-126 keeps fewer digits than y may have.  y is
+ * infinite where it is itself past its type, not where s_i w_i is.  y is rounded once to bf16;
  * q and scale are moe_quantize_fp8's format and rule on the fp32 values of y, not on their bf16
  * rounding: per run of 128 and with a = max(max_i |y_i|, 2^-100), scale = a / 448 and q_i =
  * E4M3(448 y_i / a).  A run of y that holds an infinity or a NaN gets a NaN scale and NaN elements.
@@ -50,7 +52,8 @@ moe_status moe_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* res
  * Per row, with r = 1 / sqrt(mean_j s_j^2 + eps), u = s r and z = dy w:
  *   dx_i = r (z_i - u_i mean_j(z_j u_j)) + dsum_i      (dsum NULL: without it)
  *   dweight_i = sum over rows of dy_i u_i
- * in fp32; dx is rounded once.  s is moe_rms_norm's sum, or its x where there was no residual; dx is
+ * in fp32, at any magnitude of bf16 rows as for moe_rms_norm (where r itself is past fp32's range, too);
+ * dx is rounded once.  s is moe_rms_norm's sum, or its x where there was no residual; dx is
  * then the gradient of x and of residual alike (roundings count as the identity).  dsum is
  * the gradient that reaches sum beside the norm.  The rows' order of summation in dweight depends on
  * the sizes alone.
@@ -64,7 +67,7 @@ moe_status moe_rms_norm(const uint16_t* x, int64_t x_stride, const uint16_t* res
  *   ws        moe_rms_norm_grad_workspace_bytes(rows, H) bytes, 16-byte aligned; NULL with 0 bytes
  *             will do without dweight.  Contents on entry are ignored
  * dx or dweight is given, or both (dsum needs dx).  H, s_stride and eps as for moe_rms_norm.  rows = 0
- * writes zeros to dweight.
+ * writes zeros to dweight.  A row whose mean square and eps are both 0 gives NaN.
  */
 moe_status moe_rms_norm_grad(const uint16_t* s, int64_t s_stride, int64_t rows, int32_t H,
                              int32_t weight_type, const void* weight, float eps,

@@ -12,9 +12,11 @@ constexpr int kMaxRank = 256;
 constexpr int kMaxSequences = 1 << 20;
 constexpr int kLoraMaxN = 1 << 24;
 
-// moe_rms_norm_grad: most workgroups, each of which leaves one partial row of dweight: 2^18
-// threads, whose partial rows are 8 MB at most (16 beyond H = 16384).  2^17 / 2^18 / 2^19, us: 8191 x 4096
-// 69.6 / 56.3 / 64.5, 1000 x 4096 13.8 / 13.4 / 16.8, 65536 x 128 16.5 / 16.8 / 20.1, 2048 x 16384 77.5 / 63.2 / 70.6.
+// moe_rms_norm_grad: most workgroups, each of which leaves one partial row of dweight: 2^18 threads, were a
+// row's as many as here.  The launch gives a row of 520 to 1024 elements 64 or 128 threads and one of up to 8192 512,
+// so that fewer run there.  The partial rows are 4 H bytes a workgroup: up to 8.4 MB to H = 8192, then 256 of them,
+// 16.8 MB at 16384 and 67 at 65536.  2^17 / 2^18 / 2^19, us: 8191 x 4096 with dsum 71.2 / 55.5 / 59.5, 1000 x 4096
+// 12.9 / 12.9 / 16.1, 65536 x 128 15.0 / 14.8 / 16.6, 2048 x 16384 68.2 / 52.2 / 59.5.
 inline int64_t norm_grad_groups(int64_t rows, int H) {
   int64_t threads = 256;   // of a row, or of several short ones
   while (threads < 1024 && threads * 8 < H) threads *= 2;

@@ -8,7 +8,10 @@
 //
 // Bound by latency at these sizes: 1x4096x4096 rank 16 reads 0.3 MB in one launch of 8.0 us, of which the
 // chain of offsets, rows and first loads takes about 4; 512 rows of 64 adapters read 23 MB and write 4 in
-// 7.1 and 6.4 us for the two products, whose floor at a copy's rate is 5.8 together.
+// 7.1 and 6.6 us for the two products, whose floor at a copy's rate is 5.8 together.  Ranks above 64 are
+// bound by x, read once for each 64 ranks, and by fp32 inner sums that each block of columns reads and
+// splits again: 8191x4096x4096 105 us at rank 128, 162 at 256.  Registers spill in small_kernel at 64
+// ranks (5 to 7) and in expand_kernel with fp32 results beyond 32 (3 to 19).
 #include "block.h"
 #include "block_plan.h"
 #include "lds_copy.h"
@@ -491,8 +494,8 @@ hipError_t launch_shrink(const LoraArgs& a, hipStream_t stream, int* splits) {
   const int64_t touched = a.M < a.L ? a.M : a.L;
   const int rank_blocks = (a.R + 16 * NF - 1) / (16 * NF), chunks = (a.K + 63) / 64;
   // Tiles of 64 rows need some fifty of them to fill the GPU without more splits of K than the second product
-  // reads at ease.  16 rows / 64 rows, us, 4096x4096 with 8 adapters: rank 128 2048 rows 46 / 61, 3000 69 / 59,
-  // 4096 78 / 71, 8191 142 / 106; rank 256 2048 rows 81 / 96.
+  // reads at ease.  16 rows / 64 rows, us, 4096x4096 with 8 adapters: rank 128 2048 rows 43 / 54, 3000 67 / 57,
+  // 4096 76 / 68, 8191 139 / 105; rank 256 2048 rows 73 / 84, 4096 132 / 98.
   const bool stream_rows = NF == 4 && rank_blocks > 1 && tile_bound(a.M, touched, 64) >= 48;
   const int64_t tiles = tile_bound(a.M, touched, stream_rows ? 64 : 16);
   // workgroups to fill the GPU, with four chunks of K or two a wavefront at least
@@ -533,9 +536,9 @@ hipError_t launch_add(const LoraArgs& a, int wide, hipStream_t stream) {
   const int64_t small = tile_bound(a.M, touched + 1, 16) * col_blocks;   // and the rows without an adapter
   const int nf = a.R <= 16 ? 1 : a.R <= 32 ? 2 : 4;   // fragments of 16 ranks
   // One launch where no compute unit gets a second workgroup and each one's repeat of the first product
-  // is short.  One / two launches, us: 1x4096x4096 rank 8 6.5 / 9.5, 16 7.7 / 9.1, 32 11.3 / 9.4, 64 19.8 / 12.9;
-  // 77x1003x2064 rank 32 8.9 / 10.2, 64 13.4 / 12.5; 4x256x1024 rank 64 8.6 / 11.0; 64 adapters' 64 rows of
-  // 4096x4096 (1024 workgroups) rank 16 24 / 10.6.
+  // is short.  One / two launches, us: 1x4096x4096 rank 8 7.0 / 8.0, 16 8.3 / 8.3, 32 11.7 / 9.4, 64 20.5 / 13.1;
+  // 77x1003x2064 rank 32 9.3 / 10.4, 64 13.7 / 14.1; 4x256x1024 rank 64 9.3 / 11.1; 64 adapters' 64 rows of
+  // 4096x4096 (1024 workgroups) rank 16 23.3 / 11.2.
   if (a.R <= 64 && small <= 256 && static_cast<int64_t>(16 * nf) * a.K <= 98304) {
     const dim3 grid(static_cast<unsigned>(small)), block(1024);
     if (nf == 1) small_kernel<Out, 1><<<grid, block, 0, stream>>>(a, col_blocks, wide);

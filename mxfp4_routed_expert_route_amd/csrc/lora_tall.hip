@@ -15,9 +15,10 @@
 // Bound by memory and its requests: 8191 x 4096 x 4096, rank 64, 8 adapters, moves 226 MB by the
 // counters (x, base and y once each are 201) in 54 us, 4.2 TB/s, where a copy reaches 5.1; the inner sums
 // take about 21 us of that, and with one workgroup a CU the two parts do not overlap.  MFMAs are busy
-// 0.14 of the time.  Rank 16 takes 51 us, fp32 base and y (402 MB) 85; the two launches of lora.hip 94 at
-// rank 64.  Tried without gain: 16 wavefronts (spills), columns begun at another place by each
-// workgroup, non-temporal copies of x.
+// 0.15 of the time.  Rank 16 takes 53 us, fp32 base and y (335 MB) 79 at rank 64; without a base, two
+// thirds of the bytes, 53.  A second workgroup a CU has neither LDS nor registers: a wavefront holds 202 to
+// 256, and of the fp32 form for 64 ranks one spills.  Tried without gain: 16 wavefronts (spills), columns begun
+// at another place by each workgroup, non-temporal copies of x.
 #include <atomic>
 #include <type_traits>
 

@@ -6,7 +6,7 @@
 // ones a workgroup of whole wavefronts (kLanes 0), as few threads as hold them.
 //
 // Range.  Squares of bf16 values leave fp32 beyond about 2^63 and below 2^-63.  A row whose sum of
-// squares is outside [2^-80, 2^100] is multiplied by a power of two and summed again; eps
+// squares is outside [2^-80, 2^100] is multiplied by 2^100 or 2^-74 and summed again; eps
 // goes with it.  Rows below, of zeros say, need that only if eps is as small.  Its price is one
 // comparison a row.
 #pragma once

@@ -6,12 +6,12 @@
 // whose y, or z, lies below the format's floor of 2^-100 is quantised from y.  A row whose squares are
 // too large for fp32 is multiplied by 2^-74 (norm_core.h), which its small elements must not be before
 // they meet rstd: its y are s rstd 2^-74 w, in this order.  Where s w overflows (weights of 2^78 or more),
-// what was stored is stored again, from s rstd w.  Other rows pay for that 0.2 to 0.8 us of 28 to 58 at
-// 8191 x 4096, with their elements packed until the end.
+// what was stored is stored again, from s rstd w.  Other rows pay 0.6 to 0.9 us of 27 to 58 for it at
+// 8191 x 4096: their elements stay until the results are seen.
 //
 // Bound by memory: with the residual and both outputs an element moves 9 bytes, 8191 x 4096 302 MB
-// in 57 us (5.3 TB/s, a large copy 5.1; counters show no byte read or written twice).  A single row is
-// its launch and one chain of load, sum and store: kernel 3.3 us, the host's call 5.6.
+// in 58 us (5.2 TB/s, a large copy 5.1; counters show no byte read or written twice).  A single row is
+// its launch and one chain of load, sum and store: kernel 3.4 us, the host's call 5.6.
 #include <type_traits>
 
 #include "block.h"
@@ -177,8 +177,9 @@ hipError_t launch_rms_norm(const NormArgs& a, hipStream_t stream) {
       default: return launch<64, 1>(a, stream);
     }
   }
-  // chunks a thread, 1 / 2: 8191 x 1024 18.8 us / 17.4, 8191 x 2048 31.9 / 32.5, 8191 x 4096 59.1 /
-  // 56.9, 4096 x 8192 65.7 / 58.4; 4 are slower (60.6 at 8191 x 4096)
+  // chunks a thread, 1 / 2, residual and both outputs: 8191 x 1024 15.7 us / 15.6, 8191 x 2048 31.0 / 33.4, 8191 x
+  // 4096 56.2 / 58.7 (y alone 30.8 / 28.0, E4M3 alone 34.5 / 28.4), 4096 x 8192 58.8 / 59.3 (32.5 / 29.0, 38.2 /
+  // 29.7); 4 are slower (62.2 at 8191 x 4096)
   if (a.H <= 2048) return launch<0, 1>(a, stream);
   if (a.H <= 16384) return launch<0, 2>(a, stream);
   if (a.H <= 32768) return launch<0, 4>(a, stream);

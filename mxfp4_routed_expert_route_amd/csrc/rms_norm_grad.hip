@@ -5,8 +5,11 @@
 // rows, keeps its part of dweight in registers and leaves one partial row of it, in an order that
 // the sizes alone set; a second kernel adds the partial rows.
 //
-// Bound by memory: 8191 x 4096 with dsum moves 268 MB in 55 us (4.9 TB/s; the rows 50.4, the partial rows'
-// sum 4.3).  77 x 2064 is two launches in a chain, 3.4 and 2.7 us.
+// Bound by memory: 8191 x 4096 with dsum moves 268 MB in 55 us (4.9 TB/s; the rows 51.0, the partial rows'
+// sum 4.2).  77 x 2064 is two launches in a chain, 3.4 and 2.6 us.  Beyond H = 16384 the row's parts of
+// dweight alone take the 128 registers of a lane: 33 of them spill (88 beyond 32768), and the row is read
+// twice: 1024 x 32768 with dsum 106 us for 268 MB.  At H = 1024 a row is two wavefronts, a chunk a lane, and
+// waits for its barrier: 8191 rows 19.5 us for 67 MB.
 #include "block.h"
 #include "block_plan.h"
 #include "norm_core.h"
@@ -222,8 +225,8 @@ hipError_t launch_rms_norm_grad(const NormGradArgs& a, hipStream_t stream) {
       default: return launch<64, 1>(a, stream);
     }
   }
-  // chunks a thread, 1 / 2: 8191 x 1024 27.2 us / 29.1, 8191 x 2048 34.8 / 38.0, 8191 x 4096 56.7 / 56.6,
-  // 4096 x 8192 64.7 / 61.0; the next row on its way while one is worked on gains nothing (57.4 / 56.2)
+  // chunks a thread, 1 / 2, with dsum: 8191 x 1024 20.1 us / 20.3, 8191 x 2048 33.3 / 34.1, 8191 x 4096 55.5 / 54.9,
+  // 4096 x 8192 62.1 / 61.2; the next row on its way while one is worked on gains nothing (57.4 / 56.2)
   if (a.H <= 4096) return launch<0, 1>(a, stream);
   if (a.H <= 16384) return launch<0, 2>(a, stream);
   if (a.H <= 32768) return launch<0, 4>(a, stream);
