@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+from mxfp4_routed_expert_route_amd import binding
 from oracle import block
 from tests.test_gpu_block import DEV, HALF, NORM, U, check_norm_grad, close, f64, gen, norm, norm_grad, randn
 
@@ -97,3 +98,35 @@ def test_norm_grad_of_subnormal_rows(H):
     dx, dw = norm_grad(s, w, 0.0, dy, dsum)
     check_norm_grad(s, w, 0.0, dy, dsum, dx, dw)
     assert torch.equal(dx[1], dsum[1])
+
+
+@pytest.mark.parametrize("H", SIZES)
+def test_norm_and_gradient_of_extreme_rows_in_place(H):
+    """Among ordinary rows that share their wavefronts, with outputs over inputs."""
+    g = gen(H + 4)
+    x = torch.randn(37, H, generator=g)
+    x[1::5] *= 2.0 ** -45
+    x[1::5, 2] = 2.0 ** 52
+    x[2::5] *= 2.0 ** 45        # s w overflows
+    x[3::5] *= 2.0 ** -131      # subnormal
+    x = x.bfloat16().to(DEV)
+    w = torch.randn(H, generator=g)
+    w[::7] *= 2.0 ** 90
+    w = w.to(DEV)
+    want = norm(x, w, 0.0, None, y=True, q=True)
+    y = x.clone()
+    binding.moe_rms_norm(y, w, 0.0, y=y, q=(q := torch.empty_like(want["q"])), scale=(s := torch.empty_like(want["scale"])))
+    assert torch.equal(y, want["y"]) and torch.equal(q.view(torch.uint8), want["q"].view(torch.uint8)) and torch.equal(s, want["scale"])
+    r, zero = x.clone(), torch.zeros_like(x)
+    binding.moe_rms_norm(zero, w, 0.0, residual=r, sum=r, y=zero)
+    assert torch.equal(r, x) and torch.equal(zero, want["y"])
+
+    w = randn(g, H)
+    dy, dsum = randn(g, 37, H, scale=2.0 ** -20), randn(g, 37, H)
+    dx, dw = norm_grad(x, w, 0.0, dy, dsum)
+    check_norm_grad(x, w, 0.0, dy, dsum, dx, dw)
+    ws = torch.empty(binding.moe_rms_norm_grad_workspace_bytes(37, H), dtype=torch.uint8, device=DEV)
+    for over_dy in (True, False):
+        d, e, out = dy.clone(), dsum.clone(), torch.empty(H, device=DEV)
+        binding.moe_rms_norm_grad(x, w, 0.0, d, d if over_dy else e, out, ws, dsum=e)
+        assert torch.equal(d if over_dy else e, dx) and torch.equal(out, dw)
